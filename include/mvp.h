@@ -1,7 +1,10 @@
 /*
  * mvp.h -- masked varlen prefill attention for GB300 (sm_103a), C ABI.
  *
- * Two operations, as described by the vLLM pages this library restates:
+ * Two operations, as described by the vLLM pages this library restates (and,
+ * next to them, the steps of a bounded paged cache: rotary positions written
+ * into it, first tokens that stay visible, the weight each key received, and
+ * eviction by it):
  *
  *   mvp_fill_query_ranges  -- vLLM PR #50294 review ("FA4 mm_prefix range
  *       scan -> O(1) table lookup"), "Implementation breakdown" step 1 and the
@@ -509,6 +512,58 @@ typedef struct {
 int mvp_attn_accounting(const int32_t* cu_seqlens_q, const int32_t* seq_lens_k, const int32_t* context_lens,
                         const int32_t* range_table, int num_reqs, int num_heads_q, int num_heads_kv, int head_dim,
                         int causal, int window_left, int window_right, int variant, mvp_attn_counts* out);
+
+/*
+ * Rotary positions with several axes, written into a paged K/V cache: the
+ * step before mvp_attn_fwd_paged on the same cu_seqlens_q, seq_lens_k and
+ * block_table.
+ *
+ * The first rot_dim dims of every q and k head form rot_dim / 2 pairs:
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) when adjacent = 1.  Pair i of packed
+ * row t turns by positions[axis(i)][t] * inv_freq(i) radians, (x, y) ->
+ * (x cos - y sin, x sin + y cos); the other dims are copied.  axis(i) names
+ * the coordinate the pair follows (time, height, width of an image or video
+ * token; one axis for text).  Angles are exact to 2^-32 of a turn at every
+ * int32 position; the rotation is fp32, rounded once to bf16.
+ *
+ * q, k, v       bf16 (src_fp32 = 0) or fp32 (1) [total_q, heads, head_dim]
+ *               with contiguous heads; q_stride, k_stride, v_stride elements
+ *               from one row to the next (views of one fused projection).
+ *               Base pointers and rows 16-byte aligned.
+ * q_out         bf16 [total_q, num_heads_q, head_dim] contiguous, the q of the
+ *               attention call.  May be q itself where that is bf16 and
+ *               contiguous.
+ * k_cache, v_cache  bf16 [num_blocks * block_size, num_heads_kv, head_dim].
+ *               Row i of request b is key seq_lens_k[b] - q_len_b + i (the
+ *               request's last keys), at the row of the caches that
+ *               mvp_attn_fwd_paged reads for it.  A key below 0, past the
+ *               table or in a block outside [0, num_blocks) is not written
+ *               (its query still is).
+ * positions     int32 [num_axes, total_q], num_axes 1..4; any value.
+ * rope_table    device copy of what mvp_rope_table_pack wrote, rot_dim / 2
+ *               entries of 16 bytes, 16-byte aligned.
+ * rot_dim       16 .. head_dim, a multiple of 16.  head_dim: 16 .. 512, a
+ *               multiple of 8.
+ * Rows at or past cu_seqlens_q[num_reqs] (a padded batch) are left as they
+ * were, in q_out too.
+ * Errors: MVP_ERR_ARG, MVP_ERR_UNSUPPORTED (head_dim, rot_dim, alignment),
+ * MVP_ERR_CUDA.
+ */
+int mvp_rope_append_paged(const void* q, const void* k, const void* v, int src_fp32, void* q_out, void* k_cache,
+                          void* v_cache, const int32_t* positions, const void* rope_table, int num_axes, int rot_dim,
+                          int adjacent, const int32_t* cu_seqlens_q, const int32_t* seq_lens_k,
+                          const int32_t* block_table, int block_size, int max_blocks_per_seq, int num_blocks,
+                          int num_reqs, int total_q, int num_heads_q, int num_heads_kv, int head_dim,
+                          long long q_stride, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * Host only (no CUDA call): writes the table of mvp_rope_append_paged, 16
+ * bytes per pair, into `table` (host memory).  inv_freq [pairs] radians per
+ * position, |inv_freq| <= 6; axes [pairs] the axis of each pair, below
+ * num_axes, or NULL (all 0); pairs 1..256, num_axes 1..4.
+ * Errors: MVP_ERR_ARG (then `table` may be partly written).
+ */
+int mvp_rope_table_pack(const double* inv_freq, const int32_t* axes, int pairs, int num_axes, void* table);
 
 /* Synchronises `stream`, returns MVP_ERR_DEVICE_TIMEOUT if a kernel recorded a
  * timeout since the last call (and clears it), MVP_ERR_DEVICE_BOUNDS if a

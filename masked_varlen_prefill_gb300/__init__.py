@@ -42,3 +42,8 @@ from ._lib import (  # noqa: F401
     meta_block_layout,
     meta_pack,
 )
+from ._cache import (  # noqa: F401
+    RopeTable,
+    rope_append_paged,
+    rope_table,
+)

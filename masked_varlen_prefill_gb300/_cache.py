@@ -1,0 +1,146 @@
+"""Bindings of the bounded paged cache's steps (include/mvp.h): rotary
+positions written into the cache, the weight each key received, and eviction
+by it.  Argument marshalling only, like ``_lib``.
+
+These calls run once per layer and step on small decode batches, where the
+host time of the binding is what a caller waits for; so arguments are checked
+in one pass over the tensors and pointers go to ctypes as plain integers.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import torch
+
+from ._lib import MVP_OK, MvpError, load_library
+
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+
+
+def _need(dev, dtype, **tensors):
+    """Every tensor given (not None) is contiguous, of ``dtype``, on ``dev``."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn_name, dev, stream, *args):
+    """The C call with ``dev`` current (its tensors' device) on ``stream`` or
+    the device's current stream; raises on a non-zero status."""
+    fn = getattr(load_library(), fn_name)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != MVP_OK:
+        raise MvpError(fn_name, st)
+
+
+def _caches(k_cache, v_cache, block_size):
+    """The caches as [rows, Hkv, D] and their number of blocks."""
+    if k_cache.dim() == 4:
+        k_cache = k_cache.reshape(-1, k_cache.shape[2], k_cache.shape[3])
+        v_cache = v_cache.reshape(-1, v_cache.shape[2], v_cache.shape[3])
+    if k_cache.dim() != 3 or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must be [num_blocks * block_size, Hkv, D]")
+    if block_size < 1 or k_cache.shape[0] % block_size != 0:
+        raise ValueError("cache rows must be a multiple of block_size")
+    return k_cache, v_cache, k_cache.shape[0] // block_size
+
+
+# ------------------------------------------------------------------ rotary positions
+class RopeTable:
+    """The frequencies and axes of ``rope_append_paged``'s pairs on a device
+    (``mvp_rope_table_pack``'s entries).  Made once by ``rope_table``."""
+
+    def __init__(self, entries, num_axes):
+        self.entries = entries  # int32 [pairs, 4]
+        self.num_axes = num_axes
+        self.rot_dim = 2 * entries.shape[0]
+
+
+def rope_table(inv_freq, axes=None, num_axes=None, device=None) -> RopeTable:
+    """Table of rotary pairs: ``inv_freq`` [pairs] (host, radians per position;
+    float64, so that far positions keep their angle) and ``axes`` [pairs], the
+    position axis each pair follows (None: all follow axis 0)."""
+    f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+    if f.ndim != 1 or f.shape[0] < 1:
+        raise ValueError("inv_freq must be a 1-D array of rotary pairs")
+    a = np.zeros(f.shape[0], dtype=np.int32) if axes is None else np.ascontiguousarray(np.asarray(axes, np.int32))
+    if a.shape != f.shape:
+        raise ValueError("axes must give one axis per pair")
+    if num_axes is None:
+        num_axes = int(a.max()) + 1
+    table = np.zeros((f.shape[0], 4), dtype=np.int32)
+    st = load_library().mvp_rope_table_pack(f.ctypes.data, a.ctypes.data, f.shape[0], int(num_axes), table.ctypes.data)
+    if st != MVP_OK:
+        raise MvpError("mvp_rope_table_pack", st)
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return RopeTable(torch.from_numpy(table).to(device), int(num_axes))
+
+
+def _rows_of(name, t, dtype, dev):
+    """Row stride of a [total_q, heads, D] tensor whose heads are contiguous."""
+    if t.dim() != 3 or t.device != dev or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor [total_q, heads, D] on {dev}")
+    rows, heads, d = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}'s heads must be contiguous")
+    return t.stride(0) if rows > 1 else max(t.stride(0), heads * d)
+
+
+def rope_append_paged(q, k, v, q_out, k_cache, v_cache, positions, table, cu_seqlens_q, seq_lens_k, block_table,
+                      block_size, *, adjacent=False, stream=None):
+    """Rotate q into ``q_out`` and k into the paged cache, and copy v into it
+    (see ``mvp_rope_append_paged`` in include/mvp.h): the step before
+    ``attn_fwd_paged`` with the same offsets and block table.
+
+    q [total_q, Hq, D], k/v [total_q, Hkv, D] bf16 or fp32, rows any stride
+    (views of one projection); q_out bf16 like q, contiguous; positions int32
+    [num_axes, total_q]; table a ``RopeTable``.
+    """
+    dev = _cuda_device(q_out, "q_out")
+    dtype = q.dtype
+    if dtype != _BF16 and dtype != _F32:
+        raise ValueError(f"q must be bfloat16 or float32, got {dtype}")
+    qs, ks, vs = _rows_of("q", q, dtype, dev), _rows_of("k", k, dtype, dev), _rows_of("v", v, dtype, dev)
+    k_cache, v_cache, num_blocks = _caches(k_cache, v_cache, block_size)
+    _need(dev, _BF16, q_out=q_out, k_cache=k_cache, v_cache=v_cache)
+    _need(dev, _I32, positions=positions, table=table.entries, cu_seqlens_q=cu_seqlens_q, seq_lens_k=seq_lens_k,
+          block_table=block_table)
+    total, hq, d = q.shape
+    hkv = k_cache.shape[1]
+    if q_out.shape != q.shape or k.shape != (total, hkv, d) or v.shape != k.shape or k_cache.shape[2] != d:
+        raise ValueError("q and q_out must be [total_q, Hq, D], k and v [total_q, Hkv, D], the caches [.., Hkv, D]")
+    if positions.shape != (table.num_axes, total):
+        raise ValueError(f"positions must be [{table.num_axes}, total_q]")
+    num_reqs = seq_lens_k.shape[0]
+    if cu_seqlens_q.shape != (num_reqs + 1,) or block_table.dim() != 2 or block_table.shape[0] != num_reqs:
+        raise ValueError("cu_seqlens_q must be [B + 1], seq_lens_k [B] and block_table [B, max_blocks_per_seq]")
+    _call("mvp_rope_append_paged", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype == _F32,
+          q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), table.entries.data_ptr(),
+          table.num_axes, table.rot_dim, bool(adjacent), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(),
+          block_table.data_ptr(), block_size, block_table.shape[1], num_blocks, num_reqs, total, hq, hkv, d, qs, ks,
+          vs)

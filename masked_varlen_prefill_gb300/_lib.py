@@ -40,6 +40,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 class AttnCounts(ctypes.Structure):
     """``mvp_attn_counts`` (include/mvp.h)."""
@@ -85,6 +86,9 @@ _SIGNATURES = {
     "mvp_meta_upload": (_i, [_vp, _vp]),
     "mvp_attn_fwd_varlen_scan": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i,
                                       _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
+    "mvp_rope_table_pack": (_i, [_vp, _vp, _i, _i, _vp]),
+    "mvp_rope_append_paged": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i,
+                                   _i, _i, _i, _i, _i, _ll, _ll, _ll, _vp]),
     "mvp_attn_accounting": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(AttnCounts)]),
 }
 

@@ -113,6 +113,10 @@ constexpr int kDecodeChunk = 4096;
 constexpr int kMaxSplits = 64;
 
 }  // namespace
+
+cudaError_t device_error_word(int** err, int* num_sms) { return device_state(err, num_sms); }
+void set_last_launches(int n) { g_last_launches = n; }
+
 }  // namespace mvp
 
 using namespace mvp;

@@ -7,6 +7,12 @@
 
 namespace mvp {
 
+// ----------------------------------------------------------------- host layer
+// The current device's error word, tensor-map encoder and SM count (looked up
+// once per device), and the launch count mvp_last_launch_count reports.
+cudaError_t device_error_word(int** err, int* num_sms = nullptr);
+void set_last_launches(int n);
+
 // ----------------------------------------------------------------- fill
 struct FillParams {
   const int32_t* ranges;    // [num_reqs, max_ranges, 2]

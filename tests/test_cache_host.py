@@ -1,0 +1,102 @@
+"""The bounded paged cache's steps without a GPU: the rotary table against
+exact arithmetic, the oracle's own pins, and the refusals, which return
+before anything is launched."""
+
+from fractions import Fraction
+
+import numpy as np
+import pytest
+
+import masked_varlen_prefill_gb300 as mvp
+from oracle import cache as oc
+
+A = 1 << 20  # an aligned address that nothing dereferences
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+
+    if not os.path.exists(mvp.library_path()):
+        from masked_varlen_prefill_gb300 import _build
+
+        _build.build()
+    return mvp.load_library()
+
+
+# ------------------------------------------------------------------ rotary table
+def _turns(inv):
+    """inv / (2 pi) as an exact-enough fraction (pi to 60 digits)."""
+    pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494")
+    return Fraction(inv) / (2 * pi)
+
+
+def test_rope_table_is_the_frequency_in_turns(lib):
+    inv = np.concatenate([10000.0 ** (-np.arange(64) / 64), [6.0, -1.0, 1e-9, 0.0, 2.0 ** -60]])
+    axes = (np.arange(inv.size) % 3).astype(np.int32)
+    table = np.zeros((inv.size, 4), dtype=np.uint32)
+    assert lib.mvp_rope_table_pack(inv.ctypes.data, axes.ctypes.data, inv.size, 3, table.ctypes.data) == mvp.MVP_OK
+    assert (table[:, 2] == axes).all()
+    for f, (lo, hi, _, _) in zip(inv, table.tolist()):
+        got = Fraction((hi << 32) | lo, 1 << 64)
+        err = (got - _turns(float(f))) % 1
+        assert min(err, 1 - err) <= Fraction(1, 1 << 62), f  # a position of 2^31 stays within 2^-31 of a turn
+        for pos in (1, -1, 12345, 2 ** 31 - 1, -2 ** 31):
+            turn = ((pos * ((hi << 32) | lo)) % (1 << 64)) >> 32
+            want = (pos * _turns(float(f))) % 1
+            err = (Fraction(turn, 1 << 32) - want) % 1
+            assert min(err, 1 - err) <= Fraction(1, 1 << 30)
+
+
+def test_rope_table_refusals(lib):
+    inv = np.ones(4)
+    ax = np.array([0, 1, 2, 3], dtype=np.int32)
+    out = np.zeros((4, 4), dtype=np.int32)
+    f = lib.mvp_rope_table_pack
+    assert f(None, None, 4, 1, out.ctypes.data) == mvp.MVP_ERR_ARG
+    assert f(inv.ctypes.data, None, 0, 1, out.ctypes.data) == mvp.MVP_ERR_ARG
+    assert f(inv.ctypes.data, None, 257, 1, out.ctypes.data) == mvp.MVP_ERR_ARG
+    assert f(inv.ctypes.data, ax.ctypes.data, 4, 3, out.ctypes.data) == mvp.MVP_ERR_ARG  # axis 3 of 3
+    assert f(inv.ctypes.data, None, 4, 5, out.ctypes.data) == mvp.MVP_ERR_ARG
+    for bad in (np.nan, np.inf, 6.5):
+        inv[2] = bad
+        assert f(inv.ctypes.data, None, 4, 1, out.ctypes.data) == mvp.MVP_ERR_ARG
+    with pytest.raises(ValueError):
+        mvp.rope_table([])
+    with pytest.raises(ValueError):
+        mvp.rope_table([1.0, 0.5], axes=[0])
+
+
+def _rope(lib, **over):
+    a = dict(q=A, k=A, v=A, fp32=0, q_out=A, kc=A, vc=A, pos=A, table=A, axes=1, rot=64, adj=0, cu=A, sk=A, bt=A,
+             block=16, max_blocks=4, blocks=8, reqs=1, total=4, hq=4, hkv=2, d=128, qs=512, ks=256, vs=256, stream=None)
+    a.update(over)
+    return lib.mvp_rope_append_paged(*a.values())
+
+
+def test_rope_refusals(lib):
+    for name in ("q", "k", "v", "q_out", "kc", "vc", "pos", "table", "cu", "sk", "bt"):
+        assert _rope(lib, **{name: None}) == mvp.MVP_ERR_ARG, name
+    for over in (dict(reqs=0), dict(total=-1), dict(hq=0), dict(hkv=0), dict(rot=8), dict(rot=144), dict(axes=0),
+                 dict(axes=5), dict(fp32=2), dict(adj=2), dict(block=8), dict(block=48), dict(block=512),
+                 dict(blocks=0), dict(max_blocks=0), dict(qs=511), dict(ks=255), dict(vs=0)):
+        assert _rope(lib, **over) == mvp.MVP_ERR_ARG, over
+    for over in (dict(d=100), dict(d=1024, rot=64), dict(rot=40), dict(q=A + 8), dict(k=A + 2), dict(v=A + 4),
+                 dict(q_out=A + 8), dict(kc=A + 8), dict(table=A + 8), dict(qs=516), dict(fp32=1, vs=258)):
+        assert _rope(lib, **over) == mvp.MVP_ERR_UNSUPPORTED, over
+    assert _rope(lib, total=0) == mvp.MVP_OK
+
+
+# ------------------------------------------------------------------ the oracle's own pins
+def test_oracle_rotation_keeps_lengths_and_composes():
+    rng = np.random.RandomState(0)
+    x = rng.randn(5, 2, 16)
+    inv, axes = np.array([1.0, 0.3, 0.1, 0.01]), [0, 1, 1, 0]
+    p1, p2 = rng.randint(-9, 99, (2, 5)), rng.randint(-9, 99, (2, 5))
+    for adj in (False, True):
+        y = oc.rotate(x, p1, inv, axes, adj)
+        assert np.allclose((y ** 2).sum(-1), (x ** 2).sum(-1)) and np.array_equal(y[..., 8:], x[..., 8:])
+        assert np.allclose(oc.rotate(y, p2, inv, axes, adj), oc.rotate(x, p1 + p2, inv, axes, adj))
+        assert np.allclose(oc.rotate(y, -p1, inv, axes, adj), x)
+    z = oc.rotate(np.eye(8)[:, None, :] * 1.0, np.ones((1, 8), int), [0.5] * 4, [0] * 4, False)[:, 0]
+    assert np.isclose(z[0, 0], np.cos(0.5)) and np.isclose(z[0, 4], np.sin(0.5)) and np.isclose(z[4, 0], -np.sin(0.5))
