@@ -301,6 +301,35 @@ int mvp_attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
                        size_t workspace_bytes, void* stream);
 
 /*
+ * mvp_attn_fwd_varlen / mvp_attn_fwd_paged under a sliding window that leaves
+ * the first tokens visible: keys j < first_tokens of each request are exempt
+ * from window_left, whatever the row's distance, and still bound by the
+ * causal rule (or window_right):
+ *   visible = base || rng || (j < first_tokens
+ *                             && (causal ? j <= p : window_right < 0 || j <= p + window_right))
+ * (tokens, not the per-head sink logits, which combine with them as with any
+ * other mask).  first_tokens >= 0; 0, or window_left = -1, is the plain call
+ * bit for bit.  The key tiles between the first tokens and the window are
+ * never read.  All other arguments, results and errors are those of the plain
+ * calls; MVP_ERR_ARG also for first_tokens < 0.
+ */
+int mvp_attn_fwd_varlen_first(const void* q, const void* k, const void* v, void* out, float* lse,
+                              const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, const int32_t* context_lens,
+                              int num_reqs, int total_q, int total_k, int max_q_len, int max_k_len,
+                              int num_decode_reqs, int num_heads_q, int num_heads_kv, int head_dim,
+                              const int32_t* range_table, const int32_t* range_covered, int causal, int window_left,
+                              int window_right, int first_tokens, const float* sinks, int sink_mode, float scale,
+                              void* workspace, size_t workspace_bytes, void* stream);
+int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                             const int32_t* cu_seqlens_q, const int32_t* seq_lens_k, const int32_t* block_table,
+                             int block_size, int max_blocks_per_seq, int num_blocks, const int32_t* context_lens,
+                             int num_reqs, int total_q, int max_q_len, int max_k_len, int num_decode_reqs,
+                             int num_heads_q, int num_heads_kv, int head_dim, const int32_t* range_table,
+                             const int32_t* range_covered, int causal, int window_left, int window_right,
+                             int first_tokens, const float* sinks, int sink_mode, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * Scan mode: the same attention with the request-level range list of vLLM's
  * Triton path instead of the per-row table (PR #50294 review,
  * "Implementation breakdown" 2: the (num_seqs, max_ranges, 2) tensor that

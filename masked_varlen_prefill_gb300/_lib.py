@@ -71,6 +71,10 @@ _SIGNATURES = {
                                      _vp, _vp, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp, ctypes.POINTER(AttnOptions)]),
     "mvp_attn_fwd_paged": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _i, _i, _i, _i, _i,
                                 _i, _vp, _vp, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
+    "mvp_attn_fwd_varlen_first": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                                       _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
+    "mvp_attn_fwd_paged_first": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _i, _i, _i,
+                                      _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
     "mvp_attn_fwd_varlen_static_ws": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                            _i, _i, _vp, _vp, _i, _i, _i, _vp, _i, _f, _vp]),
     "mvp_static_scratch_bytes": (_sz, []),
@@ -205,14 +209,15 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
                     context_lens=None, range_table=None, range_covered=None, causal=True, window_left=-1,
                     window_right=-1, sinks=None, sink_mode=SINK_NONE, scale=None, workspace=None,
                     num_decode_reqs=-1, stream=None, variant=VARIANT_DEFAULT, wait_limit_us=0,
-                    fault=FAULT_NONE, mixed_prefill_sms=0):
+                    fault=FAULT_NONE, mixed_prefill_sms=0, first_tokens=0):
     """Masked varlen attention forward (see ``mvp_attn_fwd_varlen``).
 
     q [total_q, Hq, D], k/v [total_k, Hkv, D] bf16; out like q; lse fp32
     [Hq, total_q] or None; cu_seqlens int32 [B+1]; the rest as in the header.
     ``variant`` / ``wait_limit_us`` / ``fault`` / ``mixed_prefill_sms`` other
     than their defaults go through ``mvp_attn_fwd_varlen_ext`` with those
-    options.
+    options.  ``first_tokens``: keys below it stay visible past
+    ``window_left`` (``mvp_attn_fwd_varlen_first``; not with those options).
     """
     lib = load_library()
     dev = q.device
@@ -240,7 +245,13 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
             hq, hkv, d, _ptr(range_table), _ptr(range_covered), int(bool(causal)), int(window_left),
             int(window_right), _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes,
             _stream(stream, dev)]
-    if variant == VARIANT_DEFAULT and wait_limit_us == 0 and fault == FAULT_NONE and mixed_prefill_sms == 0:
+    plain = variant == VARIANT_DEFAULT and wait_limit_us == 0 and fault == FAULT_NONE and mixed_prefill_sms == 0
+    if first_tokens != 0:
+        if not plain:
+            raise ValueError("first_tokens does not combine with variant, wait_limit_us, fault or mixed_prefill_sms")
+        args.insert(22, int(first_tokens))
+        name, st = "mvp_attn_fwd_varlen_first", lib.mvp_attn_fwd_varlen_first(*args)
+    elif plain:
         name, st = "mvp_attn_fwd_varlen", lib.mvp_attn_fwd_varlen(*args)
     else:
         opts = AttnOptions(int(variant), int(wait_limit_us), int(fault), int(mixed_prefill_sms))
@@ -290,11 +301,12 @@ def attn_fwd_varlen_scan(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, ma
 def attn_fwd_paged(q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_table, block_size, max_q_len,
                    max_k_len, *, lse=None, context_lens=None, range_table=None, range_covered=None, causal=True,
                    window_left=-1, window_right=-1, sinks=None, sink_mode=SINK_NONE, scale=None, workspace=None,
-                   num_decode_reqs=-1, stream=None):
+                   num_decode_reqs=-1, stream=None, first_tokens=0):
     """Masked varlen attention over a paged K/V cache (see
     ``mvp_attn_fwd_paged``): k_cache/v_cache [num_blocks * block_size, Hkv,
     D] (or [num_blocks, block_size, Hkv, D]) bf16, block_table int32 [B,
-    max_blocks_per_seq], seq_lens_k int32 [B]; the rest as ``attn_fwd_varlen``."""
+    max_blocks_per_seq], seq_lens_k int32 [B]; the rest as ``attn_fwd_varlen``
+    (``first_tokens``: ``mvp_attn_fwd_paged_first``)."""
     lib = load_library()
     dev = q.device
     if k_cache.dim() == 4:
@@ -322,14 +334,18 @@ def attn_fwd_paged(q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_tab
     if scale is None:
         scale = d ** -0.5
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib.mvp_attn_fwd_paged(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q), _ptr(seq_lens_k),
-        _ptr(block_table), int(block_size), block_table.shape[1], rows // int(block_size), _ptr(context_lens),
-        cu_seqlens_q.shape[0] - 1, total_q, int(max_q_len), int(max_k_len), int(num_decode_reqs), hq, hkv, d,
-        _ptr(range_table), _ptr(range_covered), int(bool(causal)), int(window_left), int(window_right),
-        _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes, _stream(stream, dev))
+    args = [_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q), _ptr(seq_lens_k),
+            _ptr(block_table), int(block_size), block_table.shape[1], rows // int(block_size), _ptr(context_lens),
+            cu_seqlens_q.shape[0] - 1, total_q, int(max_q_len), int(max_k_len), int(num_decode_reqs), hq, hkv, d,
+            _ptr(range_table), _ptr(range_covered), int(bool(causal)), int(window_left), int(window_right),
+            _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes, _stream(stream, dev)]
+    if first_tokens != 0:
+        args.insert(25, int(first_tokens))
+        name, st = "mvp_attn_fwd_paged_first", lib.mvp_attn_fwd_paged_first(*args)
+    else:
+        name, st = "mvp_attn_fwd_paged", lib.mvp_attn_fwd_paged(*args)
     if st != MVP_OK:
-        raise MvpError("mvp_attn_fwd_paged", st)
+        raise MvpError(name, st)
 
 
 def attn_fwd_varlen_static_ws(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_len, *, lse=None,

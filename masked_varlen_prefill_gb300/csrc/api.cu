@@ -243,7 +243,7 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
                   int causal, int window_left, int window_right, const float* sinks, int sink_mode, float scale,
                   void* workspace, size_t workspace_bytes, void* stream, const KVArgs& kv,
                   const int32_t* scan_ranges = nullptr, int max_ranges = 0,
-                  const mvp_attn_options* opts = nullptr) {
+                  const mvp_attn_options* opts = nullptr, int first_tokens = 0) {
   const void* k = kv.k;
   const void* v = kv.v;
   const bool paged = kv.block_table != nullptr;
@@ -255,6 +255,8 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   if (sink_mode != 0 && sinks == nullptr) return MVP_ERR_ARG;
   if (window_left < -1 || window_right < -1) return MVP_ERR_ARG;
   if (causal != 0 && causal != 1) return MVP_ERR_ARG;
+  if (first_tokens < 0) return MVP_ERR_ARG;
+  if (window_left < 0) first_tokens = 0;  // every past key is visible already
   if (num_decode_reqs < -1 || num_decode_reqs > num_reqs) return MVP_ERR_ARG;
   if (!(scale > 0.f) || scale > 3.0e38f) return MVP_ERR_ARG;  // NaN, <= 0, inf
   if (total_q == 0) return MVP_OK;
@@ -301,6 +303,7 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   m.causal = causal;
   m.window_left = window_left;
   m.window_right = causal ? 0 : window_right;
+  m.first_tokens = first_tokens;
   m.sink_mode = sink_mode;
   m.scale_log2 = scale * 1.4426950408889634f;
   m.scale = scale;
@@ -386,8 +389,11 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
     // Keys a decode row's CTA walks: its visible hull, started on a multiple
     // of the tile size (the kernel aligns it down by up to kt - 1 keys).
     long long span = max_k_len;
-    if (causal && window_left >= 0 && range_table == nullptr && scan_ranges == nullptr && context_lens == nullptr)
-      span = (window_left + static_cast<long long>(kt) < span) ? window_left + static_cast<long long>(kt) : span;
+    if (causal && window_left >= 0 && range_table == nullptr && scan_ranges == nullptr && context_lens == nullptr) {
+      // (and whole tiles of first tokens before it)
+      const long long first = (static_cast<long long>(first_tokens) + kt - 1) / kt * kt;
+      span = std::min(span, window_left + static_cast<long long>(kt) + first);
+    }
     int splits = static_cast<int>((span + kDecodeChunk - 1) / kDecodeChunk);
     if (splits > kMaxSplits) splits = kMaxSplits;
     const size_t per_split = static_cast<size_t>(decode_count) * num_heads_q * (head_dim + 2) * sizeof(float);
@@ -423,7 +429,9 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   if (concurrent) {
     sms = share > 0 ? share
                     : mixed_prefill_sms(num_sms, total_q, total_k, paged, paged ? kv.block_shift : 0, num_reqs,
-                                        decode_count, max_q_len, max_k_len, causal, window_left, window_right,
+                                        decode_count, max_q_len, max_k_len, causal,
+                                        window_left < 0 ? -1 : std::min(window_left, INT_MAX - first_tokens) + first_tokens,
+                                        window_right,
                                         num_heads_q, num_heads_kv);
     if (sms == 0) concurrent = false;               // too little decode work to overlap
     if (sms > num_sms - 2) sms = num_sms - 2;       // leave the decode kernel at least two SMs
@@ -491,6 +499,21 @@ int mvp_attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
                        int num_heads_kv, int head_dim, const int32_t* range_table, const int32_t* range_covered,
                        int causal, int window_left, int window_right, const float* sinks, int sink_mode, float scale,
                        void* workspace, size_t workspace_bytes, void* stream) {
+  return mvp_attn_fwd_paged_first(q, k_cache, v_cache, out, lse, cu_seqlens_q, seq_lens_k, block_table, block_size,
+                                  max_blocks_per_seq, num_blocks, context_lens, num_reqs, total_q, max_q_len,
+                                  max_k_len, num_decode_reqs, num_heads_q, num_heads_kv, head_dim, range_table,
+                                  range_covered, causal, window_left, window_right, 0, sinks, sink_mode, scale,
+                                  workspace, workspace_bytes, stream);
+}
+
+int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                             const int32_t* cu_seqlens_q, const int32_t* seq_lens_k, const int32_t* block_table,
+                             int block_size, int max_blocks_per_seq, int num_blocks, const int32_t* context_lens,
+                             int num_reqs, int total_q, int max_q_len, int max_k_len, int num_decode_reqs,
+                             int num_heads_q, int num_heads_kv, int head_dim, const int32_t* range_table,
+                             const int32_t* range_covered, int causal, int window_left, int window_right,
+                             int first_tokens, const float* sinks, int sink_mode, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   g_last_launches = 0;
   int shift = 0;
   while (shift < 30 && (1 << shift) < block_size) ++shift;
@@ -503,7 +526,23 @@ int mvp_attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
             shift, max_blocks_per_seq};
   return attn_fwd_impl(q, out, lse, cu_seqlens_q, context_lens, num_reqs, total_q, max_q_len, max_k_len,
                        num_decode_reqs, num_heads_q, num_heads_kv, head_dim, range_table, range_covered, causal,
-                       window_left, window_right, sinks, sink_mode, scale, workspace, workspace_bytes, stream, kv);
+                       window_left, window_right, sinks, sink_mode, scale, workspace, workspace_bytes, stream, kv,
+                       nullptr, 0, nullptr, first_tokens);
+}
+
+int mvp_attn_fwd_varlen_first(const void* q, const void* k, const void* v, void* out, float* lse,
+                              const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, const int32_t* context_lens,
+                              int num_reqs, int total_q, int total_k, int max_q_len, int max_k_len,
+                              int num_decode_reqs, int num_heads_q, int num_heads_kv, int head_dim,
+                              const int32_t* range_table, const int32_t* range_covered, int causal, int window_left,
+                              int window_right, int first_tokens, const float* sinks, int sink_mode, float scale,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_launches = 0;
+  KVArgs kv{k, v, total_k, cu_seqlens_k, nullptr, nullptr, 0, 0};
+  return attn_fwd_impl(q, out, lse, cu_seqlens_q, context_lens, num_reqs, total_q, max_q_len, max_k_len,
+                       num_decode_reqs, num_heads_q, num_heads_kv, head_dim, range_table, range_covered, causal,
+                       window_left, window_right, sinks, sink_mode, scale, workspace, workspace_bytes, stream, kv,
+                       nullptr, 0, nullptr, first_tokens);
 }
 
 int mvp_attn_fwd_varlen_scan(const void* q, const void* k, const void* v, void* out, float* lse,

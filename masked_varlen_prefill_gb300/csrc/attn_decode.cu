@@ -4,7 +4,8 @@
 // query (seq_len == 1) needs no mask construction: it sees a contiguous run
 // of keys.  Here such a row's visible keys are the interval
 // [max(0, p - window_left), p] (plus, in general, the range part of
-// mask.cuh), read once per KV head for all the query heads that share it.
+// mask.cuh, and the first tokens that stay visible under the window), read
+// once per KV head for all the query heads that share it.
 //
 // This path is HBM-bound (each key is 2 * D bf16 of K and V used by G query
 // heads), so it is SIMT, not tensor-core work:
@@ -165,9 +166,19 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
   // sizes and KT are powers of two), and packed and paged calls walk the
   // same tiles.
   if (lo <= hi) lo &= ~(C::KT - 1);
-  const int c_lo = lo + sp * p.chunk;
-  const int c_hi = (lo <= hi) ? min(hi, c_lo + p.chunk - 1) : -1;
-  const int n_keys = (lo <= hi && c_lo <= c_hi) ? (c_hi - c_lo + 1) : 0;
+  // First tokens that stay visible: the tiles that hold them come before the
+  // hull's in the row's walk (n_first keys, whole tiles, none of the hull's).
+  // The walk's w-th key is key w of those, then key lo + w - n_first.
+  const int f_hi = p.m.first_tokens > 0 ? first_tokens_hi(p.m, pos, k_len) : -1;
+  if (f_hi >= 0 && lo > hi) {  // nothing but first tokens
+    lo = (f_hi + C::KT) & ~(C::KT - 1);
+    hi = lo - 1;
+  }
+  const int n_first = f_hi >= 0 ? min((f_hi + C::KT) & ~(C::KT - 1), lo) : 0;
+  const int skip = lo - n_first;  // keys between the first tokens' tiles and the hull's
+  const int n_walk = (lo <= hi || n_first > 0) ? n_first + (hi - lo + 1) : 0;
+  const int w_lo = sp * p.chunk;
+  const int n_keys = max(0, min(n_walk - w_lo, p.chunk));
   const int n_tiles = (n_keys + C::KT - 1) / C::KT;
   const bool single = p.partial == nullptr;
   if (n_keys == 0 && !single) {
@@ -208,11 +219,13 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
           break;
         }
         mbar_arrive_expect_tx(&sb.full[s], 2 * C::TILE);
+        const int w0 = w_lo + t * C::KT;
+        const int key0 = w0 < n_first ? w0 : w0 + skip;
         uint8_t* ks = smem + s * 2 * C::TILE;
         uint8_t* vs = ks + C::TILE;
         // one box per run of keys inside one cache block (the whole tile when packed)
         for (int r = 0; r < C::KT; r += kbox) {
-          const int row = PAGED ? kv_row(p.m, b, k0, k_len, c_lo + t * C::KT + r) : k0 + c_lo + t * C::KT + r;
+          const int row = PAGED ? kv_row(p.m, b, k0, k_len, key0 + r) : k0 + key0 + r;
 #pragma unroll
           for (int x = 0; x < C::NBOX; ++x) {
             tma_load_3d(ks + x * (C::KT * C::BOX * 2) + r * (C::BOX * 2), &map_k, &sb.full[s], x * C::BOX, hkv, row);
@@ -275,11 +288,10 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
   const bool key0_mode = p.m.sink_mode == 1 && p.m.sinks != nullptr;
   float my_sink = 0.f;
   if (key0_mode && hh < heads_here) my_sink = __ldg(p.m.sinks + hq0 + hh) * 1.4426950408889634f;
-  // Keys every lane may take without a mask test: inside the split and in
-  // the interval the row sees whole (key 0 excluded when it carries a sink).
+  // Keys every lane may take without a mask test: in the interval the row
+  // sees whole (key 0 excluded when it carries a sink).
   int core_lo, core_hi;
   vis.core(core_lo, core_hi);
-  core_hi = min(core_hi, c_hi);
   if (key0_mode) core_lo = max(core_lo, 1);
 
   // Per-step probabilities as (p, p) pairs, [key of the step][head], read
@@ -308,7 +320,8 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
     }
     const uint8_t* ks_tile = smem + s * 2 * C::TILE;
     const uint8_t* vs_tile = ks_tile + C::TILE;
-    const int t0 = c_lo + t * C::KT;
+    const int w0 = w_lo + t * C::KT;
+    const int t0 = w0 < n_first ? w0 : w0 + skip;
     const bool interior = t0 >= core_lo && t0 + C::KT - 1 <= core_hi;
     for (int gi = warp; gi < NG; gi += C::NW) {
       float x[NSUB];
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
         if (!interior) {
           const int key = t0 + kk;
           if (key0_mode && key == 0) x[a] += my_sink;
-          if (!(key <= c_hi && vis.visible(key))) x[a] = -INFINITY;
+          if (!vis.visible(key) && key > f_hi) x[a] = -INFINITY;
         }
       }
       // max of head hh over the step's keys: this lane's NSUB, then the KS keys

@@ -128,6 +128,17 @@ __device__ __forceinline__ RowVis row_visibility_from(const MaskParams& m, int p
   return v;
 }
 
+// First tokens that stay visible under the window: the last one a query at
+// absolute position p sees ([0, hi] is visible next to the row's intervals),
+// or -1.  They are exempt from the window's past side only: the causal rule
+// (or the right window) still bounds them.
+__device__ __forceinline__ int first_tokens_hi(const MaskParams& m, int p, int k_len) {
+  long long hi = min(m.first_tokens, k_len) - 1;
+  if (m.causal) hi = min(hi, static_cast<long long>(p));
+  else if (m.window_right >= 0) hi = min(hi, static_cast<long long>(p) + m.window_right);
+  return hi < 0 ? -1 : static_cast<int>(hi);
+}
+
 // Row of a paged K/V cache (vLLM-style block table, block size
 // 2^block_shift) that holds key l of request b: the block id of l's block
 // times the block size plus l's offset in it.  Keys at or past the request's

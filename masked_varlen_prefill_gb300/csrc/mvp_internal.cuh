@@ -52,6 +52,7 @@ struct MaskParams {
   int causal;
   int window_left;           // -1 = unbounded
   int window_right;          // -1 = unbounded (non-causal only)
+  int first_tokens;          // keys [0, first_tokens) stay visible past window_left (0: none, or no window)
   int sink_mode;
   float scale_log2;          // scale * log2(e)
   float scale;               // > 0
@@ -107,6 +108,10 @@ PrefillShape prefill_tile_shape(int head_dim, bool d512_head_split);
 
 cudaError_t launch_prefill(int head_dim, bool d512_head_split, const PrefillParams& p, const CUtensorMap& map_q,
                            const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
+
+// launch_prefill's kernels for m.first_tokens > 0 (the default variants).
+cudaError_t launch_prefill_first(int head_dim, const PrefillParams& p, const CUtensorMap& map_q,
+                                 const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
 
 // ----------------------------------------------------------------- decode
 struct DecodeParams {

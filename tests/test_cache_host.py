@@ -100,3 +100,43 @@ def test_oracle_rotation_keeps_lengths_and_composes():
         assert np.allclose(oc.rotate(y, -p1, inv, axes, adj), x)
     z = oc.rotate(np.eye(8)[:, None, :] * 1.0, np.ones((1, 8), int), [0.5] * 4, [0] * 4, False)[:, 0]
     assert np.isclose(z[0, 0], np.cos(0.5)) and np.isclose(z[0, 4], np.sin(0.5)) and np.isclose(z[4, 0], -np.sin(0.5))
+
+
+def test_oracle_first_tokens_mask():
+    m = oc.mask_first(3, 8, 5, True, 1, 0, 2)  # rows at 5, 6, 7, window of two keys
+    assert [list(np.nonzero(r)[0]) for r in m] == [[0, 1, 4, 5], [0, 1, 5, 6], [0, 1, 6, 7]]
+    m = oc.mask_first(3, 8, 0, True, 0, 0, 2)  # the causal rule bounds them
+    assert [list(np.nonzero(r)[0]) for r in m] == [[0], [0, 1], [0, 1, 2]]
+    m = oc.mask_first(2, 6, 0, False, 1, 1, 4)  # and the right window
+    assert [list(np.nonzero(r)[0]) for r in m] == [[0, 1], [0, 1, 2]]
+    assert oc.mask_first(4, 9, 5, True, -1, 0, 3).sum() == oc.mask_first(4, 9, 5, True, -1, 0, 0).sum()
+    rng = np.random.RandomState(1)
+    q, k, v = rng.randn(4, 4, 8), rng.randn(9, 2, 8), rng.randn(9, 2, 8)
+    from oracle import attention as oatt
+
+    for mode in (0, 1, 2):
+        sinks = rng.randn(4)
+        a = oc.attend(q, k, v, oc.mask_first(4, 9, 5, True, 3, 0, 0), 0.3, sinks, mode)
+        b = oatt.attend_rows(np.arange(4), q, k, v, 5, True, 3, 0, None, sinks, mode, 0.3)
+        assert np.allclose(a[0], b[0]) and np.allclose(a[1], b[1])
+
+
+def test_first_tokens_refusals(lib):
+    def call(first, paged, **over):
+        a = dict(q=A, k=A, v=A, out=A, lse=None, cu_q=A, cu_k=A)
+        if paged:
+            a.update(bt=A, block=16, max_blocks=4, blocks=8)
+        a.update(ctx=None, reqs=1, total_q=4)
+        if not paged:
+            a.update(total_k=4)
+        a.update(max_q=4, max_k=4, ndec=-1, hq=4, hkv=2, d=128, table=None, covered=None, causal=1, wl=3, wr=0,
+                 first=first, sinks=None, mode=0, scale=0.1, ws=None, wsb=0, stream=None)
+        a.update(over)
+        return (lib.mvp_attn_fwd_paged_first if paged else lib.mvp_attn_fwd_varlen_first)(*a.values())
+
+    for paged in (False, True):
+        assert call(-1, paged) == mvp.MVP_ERR_ARG
+        assert call(3, paged, d=96) == mvp.MVP_ERR_UNSUPPORTED
+        assert call(3, paged, q=None) == mvp.MVP_ERR_ARG
+        assert call(3, paged, total_q=0) == mvp.MVP_OK
+    assert call(3, True, block=24) == mvp.MVP_ERR_ARG
