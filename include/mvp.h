@@ -594,6 +594,55 @@ int mvp_rope_append_paged(const void* q, const void* k, const void* v, int src_f
  */
 int mvp_rope_table_pack(const double* inv_freq, const int32_t* axes, int pairs, int num_axes, void* table);
 
+/*
+ * Eviction from a paged K/V cache by the attention weight each key received
+ * (mvp_attn_key_weights_*).  A request with n = seq_lens_k[b] <= budget keys
+ * keeps them all.  Otherwise each of its KV heads keeps, on its own, keys
+ * j < first_tokens, keys j >= n - recent_tokens, and the heaviest of the
+ * others, budget in all: ties go to the lower index, -0 and +0 are equal, NaN
+ * counts as -inf.  The kept keys keep their order and become
+ * keys 0 .. budget - 1 of that head: its K and V rows, and its weights, move
+ * there, and weights budget .. n - 1 become 0 (so keys appended there start
+ * at 0).  K and V are moved bit for bit.
+ *
+ * k_cache, v_cache  bf16 [num_blocks * block_size, num_heads_kv, head_dim],
+ *               16-byte aligned; head_dim 16 .. 512, a multiple of 8.
+ * weights       fp32 [num_slots, num_heads_kv, weight_stride], as
+ *               mvp_attn_key_weights_* leaves them; slots int32 [num_reqs],
+ *               the slot of each request (distinct), or NULL (request b's is b).
+ * weights_out   like weights, the same slots, or NULL (in place).
+ * block_table   int32 [num_reqs, max_blocks_per_seq], where the keys are.
+ * block_table_out  int32 [num_reqs, max_blocks_out], where the kept keys go,
+ *               or NULL (in place; max_blocks_out is then ignored).  A request's
+ *               entry i may be the same block in both tables; otherwise no
+ *               block of block_table_out is one of block_table, and no two
+ *               entries that are written are the same block.  (Requests that
+ *               share blocks, a common prefix, evict into blocks of their own:
+ *               in place they would overwrite each other's keys.)  A row whose
+ *               source or destination id is outside [0, num_blocks) is not
+ *               moved.
+ * seq_lens_k    int32 [num_reqs]; lengths above max_k_len count as max_k_len.
+ * new_seq_lens  int32 [num_reqs] (not seq_lens_k): min(n, budget).
+ * kept          int32 [num_reqs, num_heads_kv, budget]: the kept keys'
+ *               indices before the call, ascending; -1 past the new length.
+ * workspace     device scratch of mvp_kv_evict_workspace_size bytes, 16-byte
+ *               aligned, no initialisation needed.  Two calls that may run at
+ *               the same time need separate workspaces.
+ * Errors: MVP_ERR_ARG (also first_tokens + recent_tokens > budget, a table or
+ * weight row too short, new_seq_lens == seq_lens_k), MVP_ERR_CAPACITY
+ * (workspace too small), MVP_ERR_UNSUPPORTED (head_dim, alignment),
+ * MVP_ERR_CUDA.  num_reqs == 0: nothing is done.
+ */
+int mvp_kv_evict_paged(void* k_cache, void* v_cache, const float* weights, float* weights_out, int num_slots,
+                       long long weight_stride, const int32_t* slots, const int32_t* seq_lens_k,
+                       const int32_t* block_table, const int32_t* block_table_out, int block_size,
+                       int max_blocks_per_seq, int max_blocks_out, int num_blocks, int num_reqs, int max_k_len,
+                       int num_heads_kv, int head_dim, int budget, int first_tokens, int recent_tokens,
+                       int32_t* new_seq_lens, int32_t* kept, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mvp_kv_evict_paged needs (0 for non-positive sizes). */
+size_t mvp_kv_evict_workspace_size(int num_reqs, int num_heads_kv, int budget);
+
 /* Synchronises `stream`, returns MVP_ERR_DEVICE_TIMEOUT if a kernel recorded a
  * timeout since the last call (and clears it), MVP_ERR_DEVICE_BOUNDS if a
  * kernel of the bounds-checked build (libmvp_debug.so, compiled with

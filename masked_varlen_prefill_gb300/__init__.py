@@ -44,6 +44,8 @@ from ._lib import (  # noqa: F401
 )
 from ._cache import (  # noqa: F401
     RopeTable,
+    kv_evict_paged,
+    kv_evict_workspace_size,
     rope_append_paged,
     rope_table,
 )

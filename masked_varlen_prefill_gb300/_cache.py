@@ -144,3 +144,55 @@ def rope_append_paged(q, k, v, q_out, k_cache, v_cache, positions, table, cu_seq
           table.num_axes, table.rot_dim, bool(adjacent), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(),
           block_table.data_ptr(), block_size, block_table.shape[1], num_blocks, num_reqs, total, hq, hkv, d, qs, ks,
           vs)
+
+
+# ------------------------------------------------------------------ eviction
+def kv_evict_workspace_size(num_reqs, num_heads_kv, budget) -> int:
+    return int(load_library().mvp_kv_evict_workspace_size(num_reqs, num_heads_kv, budget))
+
+
+def _weight_args(weights, slots, num_reqs, hkv, dev, name="weights"):
+    _need(dev, _F32, **{name: weights})
+    if weights.dim() != 3 or weights.shape[1] != hkv:
+        raise ValueError(f"{name} must be [num_slots, Hkv, max_len]")
+    if slots is not None:
+        _need(dev, _I32, slots=slots)
+        if slots.shape != (num_reqs,):
+            raise ValueError("slots must be [B]")
+
+
+def kv_evict_paged(k_cache, v_cache, weights, seq_lens_k, block_table, block_size, budget, new_seq_lens, kept,
+                   workspace, max_k_len, *, first_tokens=0, recent_tokens=0, block_table_out=None, weights_out=None,
+                   slots=None, stream=None):
+    """Evict each request's keys down to ``budget`` per KV head by their
+    weights, keeping the first and the most recent ones (see
+    ``mvp_kv_evict_paged`` in include/mvp.h).
+
+    weights fp32 [num_slots, Hkv, max_len]; new_seq_lens int32 [B] and kept
+    int32 [B, Hkv, budget] are written; workspace uint8 of
+    ``kv_evict_workspace_size(B, Hkv, budget)`` bytes.  In place unless
+    ``block_table_out`` / ``weights_out`` say where the kept keys go.
+    """
+    dev = _cuda_device(k_cache, "k_cache")
+    k_cache, v_cache, num_blocks = _caches(k_cache, v_cache, block_size)
+    _need(dev, _BF16, k_cache=k_cache, v_cache=v_cache)
+    _need(dev, _I32, seq_lens_k=seq_lens_k, block_table=block_table, block_table_out=block_table_out,
+          new_seq_lens=new_seq_lens, kept=kept)
+    _need(dev, torch.uint8, workspace=workspace)
+    num_reqs, hkv, d = seq_lens_k.shape[0], k_cache.shape[1], k_cache.shape[2]
+    _weight_args(weights, slots, num_reqs, hkv, dev)
+    if weights_out is not None:
+        _need(dev, _F32, weights_out=weights_out)
+        if weights_out.shape != weights.shape:
+            raise ValueError("weights_out must be like weights")
+    for t in (block_table, block_table_out):
+        if t is not None and (t.dim() != 2 or t.shape[0] != num_reqs):
+            raise ValueError("block tables must be [B, max_blocks_per_seq]")
+    if new_seq_lens.shape != (num_reqs,) or kept.shape != (num_reqs, hkv, budget):
+        raise ValueError("new_seq_lens must be [B] and kept [B, Hkv, budget]")
+    _call("mvp_kv_evict_paged", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
+          _p(weights_out), weights.shape[0], weights.shape[2], _p(slots), seq_lens_k.data_ptr(),
+          block_table.data_ptr(), _p(block_table_out), block_size, block_table.shape[1],
+          0 if block_table_out is None else block_table_out.shape[1], num_blocks, num_reqs, max_k_len, hkv, d, budget,
+          first_tokens, recent_tokens, new_seq_lens.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
+          workspace.numel())

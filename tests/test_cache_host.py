@@ -140,3 +140,36 @@ def test_first_tokens_refusals(lib):
         assert call(3, paged, q=None) == mvp.MVP_ERR_ARG
         assert call(3, paged, total_q=0) == mvp.MVP_OK
     assert call(3, True, block=24) == mvp.MVP_ERR_ARG
+
+
+# ------------------------------------------------------------------ eviction
+def test_oracle_evict():
+    w = np.array([5, 1, 4, 4, np.nan, 4, 9, 0], dtype=np.float32)
+    assert oc.evict(w, 8, 8, 0, 0).tolist() == list(range(8))
+    assert oc.evict(w, 8, 3, 0, 0).tolist() == [0, 2, 6]  # of three equal weights the first
+    assert oc.evict(w, 8, 4, 2, 1).tolist() == [0, 1, 6, 7]
+    assert oc.evict(w, 8, 7, 0, 0).tolist() == [0, 1, 2, 3, 5, 6, 7]  # NaN goes first
+    assert oc.evict(w, 6, 3, 1, 2).tolist() == [0, 4, 5]
+
+
+def test_evict_refusals(lib):
+    def call(**over):
+        a = dict(k=A, v=A, w=A, w_out=None, slots_n=2, stride=100, slots=None, sk=A, bt=A, bt_out=None, block=16,
+                 max_blocks=8, max_out=0, blocks=20, reqs=2, max_k=100, hkv=2, d=64, budget=50, first=4, recent=10,
+                 new=A + 64, kept=A, ws=A, wsb=1 << 20, stream=None)
+        a.update(over)
+        return lib.mvp_kv_evict_paged(*a.values())
+
+    for name in ("k", "v", "w", "sk", "bt", "new", "kept", "ws"):
+        assert call(**{name: None}) == mvp.MVP_ERR_ARG, name
+    for over in (dict(reqs=-1), dict(hkv=0), dict(max_k=-1), dict(slots_n=-1), dict(budget=0), dict(first=-1),
+                 dict(recent=-1), dict(first=41), dict(block=8), dict(block=24), dict(block=512), dict(blocks=0),
+                 dict(max_blocks=6), dict(new=A), dict(stride=99), dict(slots_n=1), dict(bt_out=A, max_out=3),
+                 dict(first=2 ** 31 - 1, recent=2 ** 31 - 1)):
+        assert call(**over) == mvp.MVP_ERR_ARG, over
+    for over in (dict(d=8), dict(d=100), dict(d=520), dict(k=A + 8), dict(v=A + 2), dict(ws=A + 4)):
+        assert call(**over) == mvp.MVP_ERR_UNSUPPORTED, over
+    assert call(wsb=256) == mvp.MVP_ERR_CAPACITY
+    assert call(reqs=0) == mvp.MVP_OK
+    assert mvp.kv_evict_workspace_size(2, 3, 65) == 256 + 2 * 3 * 3 * 4
+    assert mvp.kv_evict_workspace_size(0, 3, 65) == 0
