@@ -595,6 +595,57 @@ int mvp_rope_append_paged(const void* q, const void* k, const void* v, int src_f
 int mvp_rope_table_pack(const double* inv_freq, const int32_t* axes, int pairs, int num_axes, void* table);
 
 /*
+ * The attention weight each key received: for key j of request b and KV head h
+ *   sum over the rows i of b that see key j, and over the query heads g of h,
+ *   of exp(scale * q_ig . k_jh [+ sinks[g] if j = 0, key-0-bias mode] - lse[g][i])
+ * which is the column sum of the probabilities of the attention call that
+ * wrote lse (same masks, sinks and scale; null-logit sinks enter through lse
+ * alone).  Keys that a row does not see, or that nothing sees, add 0 whatever
+ * they hold.  The sums are fp32 and the same in every run.
+ *
+ * q, k (k_cache), cu_seqlens_q .. num_decode_reqs, masks, sinks, scale: as in
+ *               mvp_attn_fwd_varlen_first / mvp_attn_fwd_paged_first.
+ *               num_heads_q / num_heads_kv at most 128.
+ * lse           fp32 [num_heads_q, total_q], read.
+ * weights       fp32 [num_slots, num_heads_kv, weight_stride], weight_stride >=
+ *               max_k_len: key j of request b is weights[slot][h][j], with slot
+ *               = slots[b] (int32 [num_reqs], distinct) or b when slots is NULL.
+ *               (By request, not by cache row: requests may share blocks.)
+ * accumulate    1: the sums are added to weights.  0: keys [0, k_len) of every
+ *               request are overwritten (0 for those without queries).  Entries
+ *               past k_len are never touched.
+ * workspace     device scratch that lets the query rows of a few long requests
+ *               be shared by more CTAs (mvp_key_weights_workspace_size), 16-byte
+ *               aligned, or NULL; no initialisation needed.  Two calls that may
+ *               run at the same time need separate workspaces.  (The number of
+ *               CTAs regroups fp32 sums: results with and without a workspace
+ *               may differ in their last bits.)
+ * Errors: MVP_ERR_ARG, MVP_ERR_UNSUPPORTED (head_dim, alignment, head ratio),
+ * MVP_ERR_CUDA.  total_q == 0: nothing to add (accumulate = 1; else
+ * MVP_ERR_ARG).
+ */
+int mvp_attn_key_weights_varlen(const void* q, const void* k, const float* lse, float* weights, int num_slots,
+                                long long weight_stride, const int32_t* slots, int accumulate,
+                                const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, const int32_t* context_lens,
+                                int num_reqs, int total_q, int total_k, int max_q_len, int max_k_len,
+                                int num_decode_reqs, int num_heads_q, int num_heads_kv, int head_dim,
+                                const int32_t* range_table, const int32_t* range_covered, int causal, int window_left,
+                                int window_right, int first_tokens, const float* sinks, int sink_mode, float scale,
+                                void* workspace, size_t workspace_bytes, void* stream);
+int mvp_attn_key_weights_paged(const void* q, const void* k_cache, const float* lse, float* weights, int num_slots,
+                               long long weight_stride, const int32_t* slots, int accumulate,
+                               const int32_t* cu_seqlens_q, const int32_t* seq_lens_k, const int32_t* block_table,
+                               int block_size, int max_blocks_per_seq, int num_blocks, const int32_t* context_lens,
+                               int num_reqs, int total_q, int max_q_len, int max_k_len, int num_decode_reqs,
+                               int num_heads_q, int num_heads_kv, int head_dim, const int32_t* range_table,
+                               const int32_t* range_covered, int causal, int window_left, int window_right,
+                               int first_tokens, const float* sinks, int sink_mode, float scale, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mvp_attn_key_weights_* can use (0: none). */
+size_t mvp_key_weights_workspace_size(int num_reqs, int num_heads_kv, int max_q_len, int max_k_len);
+
+/*
  * Eviction from a paged K/V cache by the attention weight each key received
  * (mvp_attn_key_weights_*).  A request with n = seq_lens_k[b] <= budget keys
  * keeps them all.  Otherwise each of its KV heads keeps, on its own, keys

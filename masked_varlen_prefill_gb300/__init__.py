@@ -44,6 +44,9 @@ from ._lib import (  # noqa: F401
 )
 from ._cache import (  # noqa: F401
     RopeTable,
+    attn_key_weights_paged,
+    attn_key_weights_varlen,
+    key_weights_workspace_size,
     kv_evict_paged,
     kv_evict_workspace_size,
     rope_append_paged,

@@ -146,6 +146,81 @@ def rope_append_paged(q, k, v, q_out, k_cache, v_cache, positions, table, cu_seq
           vs)
 
 
+# ------------------------------------------------------------------ weights
+def key_weights_workspace_size(num_reqs, num_heads_kv, max_q_len, max_k_len) -> int:
+    return int(load_library().mvp_key_weights_workspace_size(num_reqs, num_heads_kv, max_q_len, max_k_len))
+
+
+def _key_weights(fn_name, q, k, lse, weights, slots, accumulate, cu_seqlens_q, key_args, context_lens, max_q_len,
+                 max_k_len, total_k, num_decode_reqs, range_table, range_covered, causal, window_left, window_right,
+                 first_tokens, sinks, sink_mode, scale, workspace, stream):
+    dev = _cuda_device(q, "q")
+    _need(dev, _BF16, q=q, k=k)
+    _need(dev, _F32, lse=lse, sinks=sinks)
+    _need(dev, _I32, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens, range_table=range_table,
+          range_covered=range_covered)
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [total_q, Hq, D] and the keys [.., Hkv, D]")
+    total_q, hq, d = q.shape
+    hkv = k.shape[1]
+    num_reqs = cu_seqlens_q.shape[0] - 1
+    if lse.shape != (hq, total_q):
+        raise ValueError("lse must be [Hq, total_q]")
+    if sinks is not None and sinks.shape != (hq,):
+        raise ValueError("sinks must be [Hq]")
+    if range_table is not None and range_table.shape != (total_q, 2):
+        raise ValueError("range_table must be [total_q, 2]")
+    if context_lens is not None and context_lens.shape != (num_reqs,):
+        raise ValueError("context_lens must be [B]")
+    _weight_args(weights, slots, num_reqs, hkv, dev)
+    ws = 0
+    if workspace is not None:
+        _need(dev, torch.uint8, workspace=workspace)
+        ws = workspace.numel()
+    rows = (total_q,) if total_k is None else (total_q, total_k)
+    _call(fn_name, dev, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(), weights.data_ptr(), weights.shape[0],
+          weights.shape[2], _p(slots), bool(accumulate), cu_seqlens_q.data_ptr(), *key_args, _p(context_lens),
+          num_reqs, *rows, max_q_len, max_k_len, num_decode_reqs, hq, hkv, d, _p(range_table), _p(range_covered),
+          bool(causal), window_left, window_right, first_tokens, _p(sinks), sink_mode,
+          d ** -0.5 if scale is None else scale, _p(workspace), ws)
+
+
+def attn_key_weights_varlen(q, k, lse, weights, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_len, *, slots=None,
+                            context_lens=None, range_table=None, range_covered=None, causal=True, window_left=-1,
+                            window_right=-1, first_tokens=0, sinks=None, sink_mode=0, scale=None, accumulate=True,
+                            workspace=None, num_decode_reqs=-1, stream=None):
+    """Add (or, with ``accumulate=False``, write) the attention weight each
+    key received to ``weights`` fp32 [num_slots, Hkv, max_len]: the column
+    sums of the probabilities of the ``attn_fwd_varlen`` call with these
+    arguments that wrote ``lse`` (see ``mvp_attn_key_weights_varlen``)."""
+    dev = _cuda_device(q, "q")
+    _need(dev, _I32, cu_seqlens_k=cu_seqlens_k)
+    if cu_seqlens_k.shape != cu_seqlens_q.shape:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must be [B + 1]")
+    _key_weights("mvp_attn_key_weights_varlen", q, k, lse, weights, slots, accumulate, cu_seqlens_q,
+                 (cu_seqlens_k.data_ptr(),), context_lens, max_q_len, max_k_len, k.shape[0], num_decode_reqs,
+                 range_table, range_covered, causal, window_left, window_right, first_tokens, sinks, sink_mode, scale,
+                 workspace, stream)
+
+
+def attn_key_weights_paged(q, k_cache, lse, weights, cu_seqlens_q, seq_lens_k, block_table, block_size, max_q_len,
+                           max_k_len, *, slots=None, context_lens=None, range_table=None, range_covered=None,
+                           causal=True, window_left=-1, window_right=-1, first_tokens=0, sinks=None, sink_mode=0,
+                           scale=None, accumulate=True, workspace=None, num_decode_reqs=-1, stream=None):
+    """``attn_key_weights_varlen`` over a paged cache: the weights of the
+    ``attn_fwd_paged`` call with these arguments."""
+    dev = _cuda_device(q, "q")
+    k_cache, _, num_blocks = _caches(k_cache, k_cache, block_size)
+    _need(dev, _I32, seq_lens_k=seq_lens_k, block_table=block_table)
+    num_reqs = seq_lens_k.shape[0]
+    if cu_seqlens_q.shape != (num_reqs + 1,) or block_table.dim() != 2 or block_table.shape[0] != num_reqs:
+        raise ValueError("cu_seqlens_q must be [B + 1], seq_lens_k [B] and block_table [B, max_blocks_per_seq]")
+    _key_weights("mvp_attn_key_weights_paged", q, k_cache, lse, weights, slots, accumulate, cu_seqlens_q,
+                 (seq_lens_k.data_ptr(), block_table.data_ptr(), block_size, block_table.shape[1], num_blocks),
+                 context_lens, max_q_len, max_k_len, None, num_decode_reqs, range_table, range_covered, causal,
+                 window_left, window_right, first_tokens, sinks, sink_mode, scale, workspace, stream)
+
+
 # ------------------------------------------------------------------ eviction
 def kv_evict_workspace_size(num_reqs, num_heads_kv, budget) -> int:
     return int(load_library().mvp_kv_evict_workspace_size(num_reqs, num_heads_kv, budget))

@@ -93,6 +93,11 @@ _SIGNATURES = {
     "mvp_rope_table_pack": (_i, [_vp, _vp, _i, _i, _vp]),
     "mvp_rope_append_paged": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i,
                                    _i, _i, _i, _i, _i, _ll, _ll, _ll, _vp]),
+    "mvp_key_weights_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "mvp_attn_key_weights_varlen": (_i, [_vp, _vp, _vp, _vp, _i, _ll, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                         _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
+    "mvp_attn_key_weights_paged": (_i, [_vp, _vp, _vp, _vp, _i, _ll, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i,
+                                        _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
     "mvp_kv_evict_workspace_size": (_sz, [_i, _i, _i]),
     "mvp_kv_evict_paged": (_i, [_vp, _vp, _vp, _vp, _i, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
                                 _i, _vp, _vp, _vp, _sz, _vp]),

@@ -116,6 +116,10 @@ constexpr int kMaxSplits = 64;
 
 cudaError_t device_error_word(int** err, int* num_sms) { return device_state(err, num_sms); }
 void set_last_launches(int n) { g_last_launches = n; }
+bool encode_bf16_3d(CUtensorMap* map, const void* base, int dim, int heads, int rows, int box_x, int box_y, int box_z,
+                    bool swizzle128) {
+  return encode_3d(map, base, dim, heads, rows, box_x, box_y, box_z, swizzle128);
+}
 
 }  // namespace mvp
 

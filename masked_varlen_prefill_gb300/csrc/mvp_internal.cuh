@@ -12,6 +12,9 @@ namespace mvp {
 // once per device), and the launch count mvp_last_launch_count reports.
 cudaError_t device_error_word(int** err, int* num_sms = nullptr);
 void set_last_launches(int n);
+// TMA map of a bf16 tensor [rows, heads, dim] (after device_error_word).
+bool encode_bf16_3d(CUtensorMap* map, const void* base, int dim, int heads, int rows, int box_x, int box_y, int box_z,
+                    bool swizzle128);
 
 // ----------------------------------------------------------------- fill
 struct FillParams {

@@ -173,3 +173,51 @@ def test_evict_refusals(lib):
     assert call(reqs=0) == mvp.MVP_OK
     assert mvp.kv_evict_workspace_size(2, 3, 65) == 256 + 2 * 3 * 3 * 4
     assert mvp.kv_evict_workspace_size(0, 3, 65) == 0
+
+
+# ------------------------------------------------------------------ key weights
+def test_oracle_key_weights():
+    rng = np.random.RandomState(2)
+    q, k = rng.randn(5, 4, 8), rng.randn(9, 2, 8)
+    mask = oc.mask_first(5, 9, 4, True, 3, 0, 1)
+    sinks = rng.randn(4)
+    for mode in (0, 1, 2):
+        v = np.zeros((9, 2, 9))  # v = one-hot of the key: the output is the row of probabilities
+        v[np.arange(9), :, np.arange(9)] = 1
+        probs, lse = np.zeros((5, 4, 9)), None
+        for h in range(4):
+            o, lse = oc.attend(q[..., :], k, v[:, :, :8], mask, 0.4, sinks, mode)
+            probs[..., :8] = o
+            probs[..., 8] = oc.attend(q, k, v[:, :, 1:], mask, 0.4, sinks, mode)[0][..., 7]
+        w = oc.key_weights(q, k, lse, mask, 0.4, sinks, mode)
+        assert np.allclose(w[0], probs[:, :2].sum((0, 1))) and np.allclose(w[1], probs[:, 2:].sum((0, 1)))
+
+
+def test_key_weights_refusals(lib):
+    def call(paged, **over):
+        a = dict(q=A, k=A, lse=A, w=A, slots_n=1, stride=64, slots=None, acc=1, cu_q=A, cu_k=A)
+        if paged:
+            a.update(bt=A, block=16, max_blocks=4, blocks=8)
+        a.update(ctx=None, reqs=1, total_q=4)
+        if not paged:
+            a.update(total_k=64)
+        a.update(max_q=4, max_k=64, ndec=-1, hq=4, hkv=2, d=128, table=None, covered=None, causal=1, wl=-1, wr=-1,
+                 first=0, sinks=None, mode=0, scale=0.1, ws=None, wsb=0, stream=None)
+        a.update(over)
+        return (lib.mvp_attn_key_weights_paged if paged else lib.mvp_attn_key_weights_varlen)(*a.values())
+
+    for paged in (False, True):
+        for name in ("q", "k", "lse", "w", "cu_q", "cu_k") + (("bt",) if paged else ()):
+            assert call(paged, **{name: None}) == mvp.MVP_ERR_ARG, name
+        for over in (dict(reqs=0), dict(total_q=-1), dict(hq=3), dict(hkv=0), dict(mode=3), dict(mode=1), dict(wl=-2),
+                     dict(first=-1), dict(causal=2), dict(acc=2), dict(ndec=2), dict(scale=0.0),
+                     dict(scale=float("nan")), dict(stride=63), dict(slots_n=0), dict(max_k=0), dict(max_q=0),
+                     dict(total_q=0, acc=0)):
+            assert call(paged, **over) == mvp.MVP_ERR_ARG, over
+        for over in (dict(d=96), dict(hq=258), dict(q=A + 8), dict(k=A + 4), dict(table=A + 4)):
+            assert call(paged, **over) == mvp.MVP_ERR_UNSUPPORTED, over
+        assert call(paged, total_q=0) == mvp.MVP_OK
+    for over in (dict(block=8), dict(block=24), dict(blocks=0), dict(max_blocks=3)):
+        assert call(True, **over) == mvp.MVP_ERR_ARG, over
+    assert mvp.key_weights_workspace_size(0, 1, 1, 1) == 0
+    assert mvp.key_weights_workspace_size(4, 8, 1, 10000) == 0  # single tokens need none
