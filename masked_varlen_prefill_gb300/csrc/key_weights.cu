@@ -328,26 +328,42 @@ __global__ void __launch_bounds__(kPfThreads, PfCfg<NCH>::CTAS)
     // ---------------------------------------------------------------- column info
     bool ok = true;
     const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr;
-    for (int i = 0; ok && walk.next(); ++i) {
-      const int slot = i % kInfo;
-      // loads first, the slot's wait after them
-      float nl[4];
+    // This lane's columns lane + 32 k: row within the tile, and the lse of it.
+    int pos[4];
+    const float* src[4];
+    float sink[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = lane + 32 * k, g = c % p.group;
+      pos[k] = c < ncol ? c / p.group : INT_MAX / 2;
+      src[k] = p.lse + static_cast<size_t>(h * p.group + g) * p.m.total_q + r.q0 + c / p.group;
+      sink[k] = key0 && c < ncol ? __ldg(p.m.sinks + h * p.group + g) * kLog2e : 0.f;
+    }
+    auto load = [&](int t, float (&nl)[4]) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k, row = walk.t * p.npos + c / p.group;
-        nl[k] = -INFINITY;
-        if (c < ncol && row < r.q_len && in_bounds(r.q0 + row, p.m.total_q, p.err))
-          nl[k] = -kLog2e * __ldg(p.lse + static_cast<size_t>(h * p.group + c % p.group) * p.m.total_q + r.q0 + row);
+        const int row = t * p.npos + pos[k];
+        nl[k] = row < r.q_len && in_bounds(r.q0 + row, p.m.total_q, p.err) ? __ldg(src[k] + t * p.npos) : INFINITY;
       }
+    };
+    float nl[4], next_nl[4];
+    bool have = walk.next();
+    if (have) load(walk.t, nl);
+    for (int i = 0; ok && have; ++i) {
+      const int slot = i % kInfo, t = walk.t;
+      // the next tile's loads are in flight while this one waits for its slot
+      have = walk.next();
+      if (have) load(walk.t, next_nl);
       if (i >= kInfo) ok = mbar_wait(&sb.col_empty[slot], ((i / kInfo) - 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
       if (!__all_sync(kFull, ok)) break;
       ColInfo& f = sb.info[slot];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k, row = walk.t * p.npos + c / p.group;
-        f.nl2[c] = nl[k];
-        if (key0) f.sink[c] = c < ncol ? __ldg(p.m.sinks + h * p.group + c % p.group) * kLog2e : 0.f;
-        if (walk.ranged(walk.t)) f.rng[c] = (c < ncol && row < r.q_len) ? range_of(p.m, r, row) : make_int2(1, 0);
+        const int c = lane + 32 * k, row = t * p.npos + pos[k];
+        f.nl2[c] = -kLog2e * nl[k];
+        if (key0) f.sink[c] = sink[k];
+        if (walk.ranged(t)) f.rng[c] = row < r.q_len ? range_of(p.m, r, row) : make_int2(1, 0);
+        nl[k] = next_nl[k];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sb.col_full[slot]);
