@@ -605,7 +605,7 @@ int mvp_rope_table_pack(const double* inv_freq, const int32_t* axes, int pairs, 
  *
  * q, k (k_cache), cu_seqlens_q .. num_decode_reqs, masks, sinks, scale: as in
  *               mvp_attn_fwd_varlen_first / mvp_attn_fwd_paged_first.
- *               num_heads_q / num_heads_kv at most 128.
+ *               num_heads_q / num_heads_kv at most 128, scale at least 1e-30.
  * lse           fp32 [num_heads_q, total_q], read.
  * weights       fp32 [num_slots, num_heads_kv, weight_stride], weight_stride >=
  *               max_k_len: key j of request b is weights[slot][h][j], with slot
@@ -620,8 +620,8 @@ int mvp_rope_table_pack(const double* inv_freq, const int32_t* axes, int pairs, 
  *               run at the same time need separate workspaces.  (The number of
  *               CTAs regroups fp32 sums: results with and without a workspace
  *               may differ in their last bits.)
- * Errors: MVP_ERR_ARG, MVP_ERR_UNSUPPORTED (head_dim, alignment, head ratio),
- * MVP_ERR_CUDA.  total_q == 0: nothing to add (accumulate = 1; else
+ * Errors: MVP_ERR_ARG, MVP_ERR_UNSUPPORTED (head_dim, alignment, head ratio,
+ * scale), MVP_ERR_CUDA.  total_q == 0: nothing to add (accumulate = 1; else
  * MVP_ERR_ARG).
  */
 int mvp_attn_key_weights_varlen(const void* q, const void* k, const float* lse, float* weights, int num_slots,

@@ -11,17 +11,23 @@
 // own columns in fp32 registers, and nothing is reduced across threads.  No
 // atomics: the sums are the same in every run.
 //
-// Prefill rows: a CTA keeps a 128-key block of one KV head in shared memory
-// (the A operand, loaded once) and streams the query tiles that see any of it,
-// 128 columns = 128 / G positions x G heads, through a ring of 64-dim chunks
-// (the B operand).  Work: 2 D flops and one exponential per visible (row, key)
-// and head; at D = 128 the exponentials (16384 per 128 x 128 tile) cost as much
-// as the MMA, so both must overlap: S^T is double-buffered in TMEM, one thread
-// issues the MMAs, two warpgroups of epilogue warps split each tile's columns.
-// Visibility is a closed interval of columns per key (the causal and window
-// rules solved for the row), so a masked tile costs one bit mask per 32
-// columns; tiles seen whole skip it.  Only range-table rows need a test per
-// column, in the tiles that hold such a row.
+// Prefill rows: a CTA pair (.cta_group::2 MMAs, M = 256) keeps a 256-key block
+// of one KV head in shared memory (the A operand, each CTA its 128 keys) and
+// streams the query tiles that see any of it, N = 256 columns = 2 x floor(128 /
+// G) positions x G heads, each CTA loading half of them, through a ring of
+// 64-dim chunks (the B operand).  S^T is double-buffered in TMEM; two
+// warpgroups of epilogue warps per CTA each take half of a tile's columns.
+// * -lse / scale is added by the tensor core: 16 more dims, three of them the
+//   bf16 terms of it (hi + mid + lo, 24 bits) in the columns' operand against
+//   ones in the keys'.  Read from shared memory instead it cost a wavefront per
+//   column and warp (with operands and copies the shared-memory pipe was full).
+// * Work: 2 D flops and one exponential per visible (row, key) and head; the
+//   exponentials (32 per clock and SM) take half the MMA's time at D = 256 and
+//   as long at D = 128.
+// * Visibility is a closed interval of columns per key (the causal and window
+//   rules solved for the row), so a masked tile costs one bit mask per 32
+//   columns; tiles seen whole skip it.  Only range-table rows need a test per
+//   column, in the tiles that hold such a row.
 //
 // Single-token rows: K is streamed (the A operand, 64-dim chunks of 128 keys),
 // the row's G heads are the B operand (N = G rounded up to 16); bound by the
@@ -51,7 +57,7 @@ struct KwParams {
   MaskParams m;
   const float* lse;        // [hq, total_q]
   float* w;                // [num_slots, hkv, w_stride]
-  float* partial;          // [splits, num_reqs, hkv, n_kb * 128] or null (one split)
+  float* partial;          // [splits, num_reqs, hkv, n_kb * 256] or null (one split)
   const int32_t* slots;    // or null
   int num_slots;
   long long w_stride;
@@ -61,6 +67,7 @@ struct KwParams {
   int skip_decode;         // prefill kernel: leave single-token requests
   int npos;                // query positions per tile
   int n_kb;                // key blocks (prefill) or key chunks (decode) of max_k_len
+  int blocks;              // key blocks one CTA pair takes, one after the other
   int splits;              // parts the query tiles of a key block are shared by
   int max_k_len;
   int* err;
@@ -113,39 +120,45 @@ __device__ __forceinline__ int2 range_of(const MaskParams& m, const Req& r, int 
 // ------------------------------------------------------------------ prefill rows
 constexpr int kPfThreads = 384;  // producer, MMA, column and idle warps, 8 epilogue warps
 constexpr int kMaxTileBits = 4096;
-constexpr int kInfo = 4;  // column-info slots
+constexpr int kTile = 2 * kCols;           // columns of a pair's tile
+constexpr int kExtBytes = kCols * 32;      // 128 rows x 16 dims of bf16
+constexpr float kHuge = 3.0e38f;           // (a bf16 value near it stays finite)
 
 template <int NCH>
 struct PfCfg {
-  static constexpr int STAGES = NCH <= 2 ? 4 : (NCH == 4 ? 8 : 5);  // Q chunks in flight
+  static constexpr int KBUF = NCH <= 4 ? 2 : 1;                  // K blocks in shared memory
+  static constexpr int STAGES = NCH <= 2 ? 8 : 5;                // Q chunks in flight
   static constexpr int K_BYTES = NCH * kChunkBytes;
-  static constexpr int SMEM = K_BYTES + STAGES * kChunkBytes + 1024;
-  static constexpr int CTAS = SMEM <= 110 * 1024 ? 2 : 1;
+  static constexpr int Q_OFF = KBUF * K_BYTES;
+  static constexpr int EXT_OFF = Q_OFF + STAGES * kChunkBytes;   // ones, then two slots
+  static constexpr int RNG_OFF = EXT_OFF + 3 * kExtBytes;        // two slots of kTile intervals
+  static constexpr int SHARED_OFF = RNG_OFF + 2 * kTile * 8;
 };
 
-struct ColInfo {
-  float nl2[kCols];   // -lse * log2(e); -inf for columns without a row
-  float sink[kCols];  // key-0 sinks in log2 units (key-0 mode)
-  int2 rng[kCols];    // range interval of the column's row (tiles with ranges)
-};
-
-template <int NCH>
 struct __align__(16) PfShared {
-  ColInfo info[kInfo];
   uint32_t range_bits[kMaxTileBits / 32];  // tiles with a row whose range meets this key block
   float part[kKeys];                       // second epilogue warpgroup's sums
-  uint64_t k_full;
+  float sink[kCols];                       // key-0 sinks of a CTA's columns, log2 units
+  uint64_t k_full[2], k_empty[2];
   uint64_t q_full[8], q_empty[8];
+  uint64_t ext_full[2];
   uint64_t s_full[2], s_empty[2];
-  uint64_t col_full[kInfo], col_empty[kInfo];
+  uint64_t rng_full[2], rng_empty[2];
   uint64_t final_mma;
   uint32_t tmem_base;
   WaitCtl wc;
 };
+template <int NCH>
+constexpr int pf_smem() {
+  return PfCfg<NCH>::SHARED_OFF + static_cast<int>(sizeof(PfShared)) + 1024;
+}
+static_assert(pf_smem<4>() <= 227 * 1024 && pf_smem<8>() <= 227 * 1024 && pf_smem<2>() <= 227 * 1024, "smem budget");
 
-// The query tiles a CTA visits: [t_lo, t_hi) by the closed-form rules and, with
-// a range table, the earlier ones whose bit is set; every role walks them alike.
+// Key block of the pair, and the query tiles that see any of it: [t_lo, t_hi)
+// by the closed-form rules and, with a range table, the earlier ones whose bit
+// is set.  Every role of both CTAs walks them alike.
 struct TileWalk {
+  int ja, jb;            // keys of the block
   int t, t_lo, t_hi;
   const uint32_t* bits;  // null: no ranges
   bool all;              // more tiles than bits: visit every one
@@ -159,77 +172,102 @@ struct TileWalk {
   }
 };
 
+// bits: the block's range bits, or null; whole: before the split.
+__device__ __forceinline__ TileWalk walk_of(const KwParams& p, const Req& r, int kb, int split, const uint32_t* bits,
+                                            bool whole) {
+  TileWalk w;
+  w.ja = kb * kTile;
+  w.jb = min(w.ja + kTile, r.k_len) - 1;
+  const int rows = 2 * p.npos, n_tiles = (r.q_len + rows - 1) / rows;
+  long long lo_a, hi_a, lo_b, hi_b;
+  seen_by(p.m, w.ja, lo_a, hi_a);
+  seen_by(p.m, w.jb, lo_b, hi_b);
+  // positions [lo of the first key, hi of the last] (a first token's hi is unbounded)
+  const long long lo = max(lo_a - r.ctx, 0LL), hi = min(max(hi_a, hi_b) - r.ctx, static_cast<long long>(r.q_len) - 1);
+  w.t_lo = static_cast<int>(min(lo / rows, static_cast<long long>(n_tiles)));
+  w.t_hi = hi < 0 ? 0 : static_cast<int>(hi / rows) + 1;
+  w.bits = bits;
+  w.all = n_tiles > kMaxTileBits;
+  w.t = -1;
+  if (w.jb < w.ja) w.t_hi = 0;
+  if (!whole) {
+    const int first = bits != nullptr ? 0 : w.t_lo;
+    const long long n = max(w.t_hi - first, 0);
+    const int a = first + static_cast<int>(n * split / p.splits);
+    w.t_hi = first + static_cast<int>(n * (split + 1) / p.splits);
+    w.t_lo = max(w.t_lo, a);
+    w.t = a - 1;
+  }
+  return w;
+}
+
+// Descriptor of an operand of 16 dims without swizzle: 8-row x 16-byte core
+// matrices, the two along K 128 bytes apart, the row groups 256.
+__device__ __forceinline__ uint64_t ext_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+         (static_cast<uint64_t>(256 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+// Byte offset of dims 8 * half .. + 7 of a row in it.
+__device__ __forceinline__ int ext_off(int row, int half) { return (row >> 3) * 256 + half * 128 + (row & 7) * 16; }
+
 template <int NCH, bool PAGED>
-__global__ void __launch_bounds__(kPfThreads, PfCfg<NCH>::CTAS)
+__global__ void __launch_bounds__(kPfThreads, 1)
     key_weights_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                                const KwParams p) {
   using C = PfCfg<NCH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
-  uint8_t* sQ = smem + C::K_BYTES;
-  __shared__ PfShared<NCH> sb;
+  uint8_t* sQ = smem + C::Q_OFF;
+  uint8_t* sE = smem + C::EXT_OFF;
+  int2* sR = reinterpret_cast<int2*>(smem + C::RNG_OFF);
+  PfShared& sb = *reinterpret_cast<PfShared*>(smem + C::SHARED_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
 
   griddep_wait();
-  int x = blockIdx.x;
-  const int kb = x % p.n_kb;
-  x /= p.n_kb;
+  int x = blockIdx.x >> 1;
+  const int n_groups = (p.n_kb + p.blocks - 1) / p.blocks;
+  const int kb0 = (x % n_groups) * p.blocks;
+  x /= n_groups;
   const int split = x % p.splits;
   x /= p.splits;
   const int h = x % p.hkv;
   const int b = x / p.hkv + p.req_offset;
   const Req r = load_req<PAGED>(p, b);
-  const int ja = kb * kKeys, jb = min(ja + kKeys, r.k_len) - 1;
-  if (jb < ja || (p.skip_decode && r.q_len == 1)) return;
+  if (kb0 * kTile >= r.k_len || (p.skip_decode && r.q_len == 1)) return;  // (both CTAs)
+  const int kb1 = min(kb0 + p.blocks, (r.k_len + kTile - 1) / kTile);
   const bool use_table = table_active(p.m);
+  const uint32_t* bits = use_table ? sb.range_bits : nullptr;
+  const int ncol = p.npos * p.group;  // columns of a CTA's half of a tile that have rows
 
-  // Tiles by the closed-form rules: positions [lo of the first key, hi of the
-  // last], where a first token's hi is unbounded.
-  TileWalk walk;
-  const int n_tiles = (r.q_len + p.npos - 1) / p.npos;
-  {
-    long long lo_a, hi_a, lo_b, hi_b;
-    seen_by(p.m, ja, lo_a, hi_a);
-    seen_by(p.m, jb, lo_b, hi_b);
-    const long long lo = max(lo_a - r.ctx, 0LL), hi = min(max(hi_a, hi_b) - r.ctx, static_cast<long long>(r.q_len) - 1);
-    walk.t_lo = static_cast<int>(min(lo / p.npos, static_cast<long long>(n_tiles)));
-    walk.t_hi = hi < 0 ? 0 : static_cast<int>(hi / p.npos) + 1;
-    walk.bits = use_table ? sb.range_bits : nullptr;
-    walk.all = n_tiles > kMaxTileBits;
-  }
-  if (use_table && !walk.all) {
-    for (int i = threadIdx.x; i < kMaxTileBits / 32; i += kPfThreads) sb.range_bits[i] = 0;
-    __syncthreads();
-    const int rows = min(walk.t_hi * p.npos, r.q_len);
-    for (int i = threadIdx.x; i < rows; i += kPfThreads) {
-      const int2 e = range_of(p.m, r, i);
-      if (max(e.x, ja) <= min(e.y, jb)) atomicOr(&sb.range_bits[(i / p.npos) >> 5], 1u << ((i / p.npos) & 31));
+  // Tiles whose ranges meet the key block (with a table, one block per pair).
+  if (use_table) {
+    const TileWalk w = walk_of(p, r, kb0, 0, bits, true);
+    if (!w.all) {
+      for (int i = threadIdx.x; i < kMaxTileBits / 32; i += kPfThreads) sb.range_bits[i] = 0;
+      __syncthreads();
+      const int rows = min(w.t_hi * 2 * p.npos, r.q_len);
+      for (int i = threadIdx.x; i < rows; i += kPfThreads) {
+        const int2 e = range_of(p.m, r, i);
+        const int t = i / (2 * p.npos);
+        if (max(e.x, w.ja) <= min(e.y, w.jb)) atomicOr(&sb.range_bits[t >> 5], 1u << (t & 31));
+      }
     }
   }
-  // This split's part of the tiles (the closed-form ones and those before).
-  {
-    const int first = use_table ? 0 : walk.t_lo;
-    const long long n = max(walk.t_hi - first, 0);
-    const int a = first + static_cast<int>(n * split / p.splits), e = first + static_cast<int>(n * (split + 1) / p.splits);
-    walk.t_hi = e;
-    walk.t_lo = max(walk.t_lo, a);
-    walk.t = a - 1;
-  }
-
   if (threadIdx.x == 0) {
-    mbar_init(&sb.k_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sb.k_full[i], 1);
+      mbar_init(&sb.k_empty[i], 1);
+      mbar_init(&sb.ext_full[i], 2);   // both CTAs' column warps
+      mbar_init(&sb.s_full[i], 1);
+      mbar_init(&sb.s_empty[i], 16);   // both CTAs' epilogue warps (rank 0's barrier)
+      mbar_init(&sb.rng_full[i], 1);
+      mbar_init(&sb.rng_empty[i], 8);
+    }
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&sb.q_full[i], 1);
       mbar_init(&sb.q_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sb.s_full[i], 1);
-      mbar_init(&sb.s_empty[i], 8);
-    }
-    for (int i = 0; i < kInfo; ++i) {
-      mbar_init(&sb.col_full[i], 1);
-      mbar_init(&sb.col_empty[i], 8);
     }
     mbar_init(&sb.final_mma, 1);
     sb.wc.abort = 0;
@@ -237,237 +275,310 @@ __global__ void __launch_bounds__(kPfThreads, PfCfg<NCH>::CTAS)
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&sb.tmem_base, 2 * kCols);
-    tmem_relinquish();
+    tmem_alloc_pair(&sb.tmem_base, 2 * kTile);
+    tmem_relinquish_pair();
   }
-  // Rows of a Q chunk that no copy writes (128 is not a multiple of the group):
-  // zero, so that their columns are finite.
-  const int ncol = p.npos * p.group;
+  // Operand parts that nothing else writes: ones in the first three dims of the
+  // keys' extension, zeros in dims 8 .. 15 of the columns', and zeros in the
+  // rows of a Q chunk past the last column.
+  for (int i = threadIdx.x; i < kCols; i += kPfThreads) {
+    *reinterpret_cast<uint4*>(sE + ext_off(i, 0)) = make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u);
+    *reinterpret_cast<uint4*>(sE + ext_off(i, 1)) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(sE + kExtBytes + ext_off(i, 1)) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(sE + 2 * kExtBytes + ext_off(i, 1)) = make_uint4(0, 0, 0, 0);
+    const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr && i < ncol;
+    sb.sink[i] = key0 ? __ldg(p.m.sinks + h * p.group + i % p.group) * kLog2e : 0.f;
+  }
   if (ncol < kCols) {
     const int words = (kCols - ncol) * 8;  // 16-byte words at the end of each chunk
     for (int i = threadIdx.x; i < C::STAGES * words; i += kPfThreads)
       reinterpret_cast<uint4*>(sQ + (i / words) * kChunkBytes + ncol * 128)[i % words] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
   }
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // the peer's barriers and operand parts are there
   tc_fence_after();
   const uint32_t tmem = sb.tmem_base;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
+    // Each CTA loads its 128 keys of a block and its half of a tile's columns;
+    // both complete on rank 0's barriers.
     if (lane == 0) {
       bool ok = true;
-      int n = 0;  // chunks issued
-      bool k_loaded = false;
+      int n = 0, nb = 0;  // Q chunks, K blocks issued
       const uint32_t q_bytes = static_cast<uint32_t>(ncol) * 128;
-      while (ok && walk.next()) {
-        if (!k_loaded) {
-          k_loaded = true;
-          mbar_arrive_expect_tx(&sb.k_full, C::K_BYTES);
-          const int run = PAGED ? min(kKeys, 1 << p.m.block_shift) : kKeys;
-          for (int i = 0; i < kKeys; i += run) {
-            const int row = PAGED ? kv_row(p.m, b, 0, r.k_len, ja + i) : r.k0 + ja;
+      const int run = PAGED ? min(kKeys, 1 << p.m.block_shift) : kKeys;
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
+        TileWalk walk = walk_of(p, r, kb, split, bits, false);
+        bool k_loaded = false;
+        while (ok && walk.next()) {
+          if (!k_loaded) {
+            k_loaded = true;
+            const int s = nb % C::KBUF;
+            if (nb >= C::KBUF && !mbar_wait(&sb.k_empty[s], ((nb / C::KBUF) - 1) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&sb.k_full[s], 2 * C::K_BYTES);
+            const uint32_t bar = mapa_shared(smem_u32(&sb.k_full[s]), 0);
+            for (int i = 0; i < kKeys; i += run) {
+              const int key = walk.ja + rank * kKeys + i;
+              const int row = PAGED ? kv_row(p.m, b, 0, r.k_len, key) : r.k0 + key;
 #pragma unroll
-            for (int c = 0; c < NCH; ++c)
-              tma_load_3d(sK + c * kChunkBytes + i * 128, &map_k, &sb.k_full, c * 64, h, row);
+              for (int c = 0; c < NCH; ++c)
+                tma_load_3d_pair(sK + s * C::K_BYTES + c * kChunkBytes + i * 128, &map_k, bar, c * 64, h, row);
+            }
+            ++nb;
           }
-        }
-        for (int c = 0; ok && c < NCH; ++c, ++n) {
-          const int s = n % C::STAGES;
-          if (n >= C::STAGES && !mbar_wait(&sb.q_empty[s], ((n / C::STAGES) - 1) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
-            ok = false;
-            break;
+          const int q_row = r.q0 + (2 * walk.t + rank) * p.npos;
+          for (int c = 0; c < NCH; ++c, ++n) {
+            const int s = n % C::STAGES;
+            if (n >= C::STAGES && !mbar_wait(&sb.q_empty[s], ((n / C::STAGES) - 1) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&sb.q_full[s], 2 * q_bytes);
+            tma_load_3d_pair(sQ + s * kChunkBytes, &map_q, mapa_shared(smem_u32(&sb.q_full[s]), 0), c * 64, h * p.group,
+                             q_row);
           }
-          mbar_arrive_expect_tx(&sb.q_full[s], q_bytes);
-          tma_load_3d(sQ + s * kChunkBytes, &map_q, &sb.q_full[s], c * 64, h * p.group, r.q0 + walk.t * p.npos);
         }
       }
       if (!ok) sb.wc.abort = 1;
-      WaitCtl own = own_wait_ctl(&sb.wc);  // copies in flight complete before the CTA leaves
-      if (k_loaded) mbar_wait(&sb.k_full, 0, &own, nullptr, 0);
-      for (int s = 0; s < C::STAGES && s < n; ++s) mbar_wait(&sb.q_full[s], ((n - 1 - s) / C::STAGES) & 1, &own, nullptr, 0);
+      // Copies in flight complete before the CTAs leave (rank 1 stays until
+      // rank 0 has drained: the final cluster barrier).
+      if (rank == 0) {
+        WaitCtl own = own_wait_ctl(&sb.wc);
+        for (int s = 0; s < C::KBUF && s < nb; ++s) mbar_wait(&sb.k_full[s], ((nb - 1 - s) / C::KBUF) & 1, &own, nullptr, 0);
+        for (int s = 0; s < C::STAGES && s < n; ++s) mbar_wait(&sb.q_full[s], ((n - 1 - s) / C::STAGES) & 1, &own, nullptr, 0);
+      }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- MMAs
-    constexpr uint32_t idesc = idesc_bf16_f32(kKeys, kCols, false, false);
-    const uint64_t dk = smem_desc_sw128(smem_u32(sK), 16, 1024);
+    constexpr uint32_t idesc = idesc_bf16_f32(2 * kKeys, kTile, false, false);
+    const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t ones = ext_desc(smem_u32(sE)), ext = ext_desc(smem_u32(sE + kExtBytes));
     const bool issuer = elect_one();
     bool ok = true;
-    int n = 0;  // chunks
-    for (int i = 0; ok && walk.next(); ++i) {
-      if (i == 0) ok = mbar_wait(&sb.k_full, 0, &sb.wc, p.err, kDevTimeoutLoad);
-      if (ok && i >= 2) ok = mbar_wait(&sb.s_empty[i & 1], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutSoftmax);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (i & 1) * kCols;
-      for (int c = 0; c < NCH; ++c, ++n) {
-        const int s = n % C::STAGES;
-        if (!mbar_wait_spin(&sb.q_full[s], (n / C::STAGES) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
-          ok = false;
-          break;
-        }
-        if (issuer) {
+    int n = 0, nb = 0, i = 0;  // chunks, K blocks, tiles
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
+      TileWalk walk = walk_of(p, r, kb, split, bits, false);
+      bool any = false;
+      for (; ok && walk.next(); ++i) {
+        const int ks = nb % C::KBUF;
+        if (!any) ok = mbar_wait(&sb.k_full[ks], (nb / C::KBUF) & 1, &sb.wc, p.err, kDevTimeoutLoad);
+        any = true;
+        if (ok && i >= 2) ok = mbar_wait_cluster(&sb.s_empty[i & 1], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutSoftmax);
+        if (ok) ok = mbar_wait_cluster(&sb.ext_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (i & 1) * kTile;
+        const uint64_t dk = desc_add(dk0, static_cast<uint32_t>((ks * C::K_BYTES) >> 4));
+        if (issuer) mma_ss_one<2>(d, ones, desc_add(ext, static_cast<uint32_t>(((i & 1) * kExtBytes) >> 4)), idesc, 0u);
+        for (int c = 0; c < NCH; ++c, ++n) {
+          const int s = n % C::STAGES;
+          if (!mbar_wait_spin(&sb.q_full[s], (n / C::STAGES) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
+            ok = false;
+            break;
+          }
+          if (issuer) {
 #pragma unroll
-          for (int k16 = 0; k16 < 4; ++k16)
-            mma_ss_one<1>(d, desc_add(dk, static_cast<uint32_t>((c * kChunkBytes + k16 * 32) >> 4)),
-                          desc_add(dq, static_cast<uint32_t>((s * kChunkBytes + k16 * 32) >> 4)), idesc,
-                          (c | k16) != 0 ? 1u : 0u);
+            for (int k16 = 0; k16 < 4; ++k16)
+              mma_ss_one<2>(d, desc_add(dk, static_cast<uint32_t>((c * kChunkBytes + k16 * 32) >> 4)),
+                            desc_add(dq, static_cast<uint32_t>((s * kChunkBytes + k16 * 32) >> 4)), idesc, 1u);
+          }
+          __syncwarp();
+          mma_commit_elect<2>(&sb.q_empty[s]);
         }
-        __syncwarp();
-        mma_commit_elect<1>(&sb.q_empty[s]);
+        if (ok) mma_commit_elect<2>(&sb.s_full[i & 1]);
       }
-      if (ok) mma_commit_elect<1>(&sb.s_full[i & 1]);
+      if (any) {
+        if (ok) mma_commit_elect<2>(&sb.k_empty[nb % C::KBUF]);
+        ++nb;
+      }
     }
     if (!ok && lane == 0) sb.wc.abort = 1;
-    mma_commit_elect<1>(&sb.final_mma);
+    mma_commit_elect<2>(&sb.final_mma);
     WaitCtl own = own_wait_ctl(&sb.wc);
     mbar_wait(&sb.final_mma, 0, &own, p.err, kDevTimeoutMma);
   } else if (warp == 2) {
-    // ---------------------------------------------------------------- column info
+    // ---------------------------------------------------------------- columns
+    // This lane's columns lane + 32 k of the CTA's half: row within the tile,
+    // and the lse of it.  -lse / scale goes into the column's extension as
+    // three bf16 terms.
     bool ok = true;
-    const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr;
-    // This lane's columns lane + 32 k: row within the tile, and the lse of it.
     int pos[4];
     const float* src[4];
-    float sink[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int c = lane + 32 * k, g = c % p.group;
-      pos[k] = c < ncol ? c / p.group : INT_MAX / 2;
-      src[k] = p.lse + static_cast<size_t>(h * p.group + g) * p.m.total_q + r.q0 + c / p.group;
-      sink[k] = key0 && c < ncol ? __ldg(p.m.sinks + h * p.group + g) * kLog2e : 0.f;
+      const int c = lane + 32 * k;
+      pos[k] = c < ncol ? rank * p.npos + c / p.group : INT_MAX / 2;
+      src[k] = p.lse + static_cast<size_t>(h * p.group + c % p.group) * p.m.total_q + r.q0 + rank * p.npos + c / p.group;
     }
-    auto load = [&](int t, float (&nl)[4]) {
+    auto load = [&](int t, float (&l)[4]) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int row = t * p.npos + pos[k];
-        nl[k] = row < r.q_len && in_bounds(r.q0 + row, p.m.total_q, p.err) ? __ldg(src[k] + t * p.npos) : INFINITY;
+        const int row = 2 * t * p.npos + pos[k];
+        l[k] = row < r.q_len && in_bounds(r.q0 + row, p.m.total_q, p.err) ? __ldg(src[k] + 2 * t * p.npos) : INFINITY;
       }
     };
-    float nl[4], next_nl[4];
-    bool have = walk.next();
-    if (have) load(walk.t, nl);
-    for (int i = 0; ok && have; ++i) {
-      const int slot = i % kInfo, t = walk.t;
-      // the next tile's loads are in flight while this one waits for its slot
-      have = walk.next();
-      if (have) load(walk.t, next_nl);
-      if (i >= kInfo) ok = mbar_wait(&sb.col_empty[slot], ((i / kInfo) - 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
-      if (!__all_sync(kFull, ok)) break;
-      ColInfo& f = sb.info[slot];
+    const float inv = -1.f / p.m.scale;
+    const uint32_t ext_bar = mapa_shared(smem_u32(&sb.ext_full[0]), 0);
+    int i = 0;
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
+      TileWalk walk = walk_of(p, r, kb, split, bits, false);
+      float l[4], next_l[4];
+      bool have = walk.next();
+      if (have) load(walk.t, l);
+      for (; ok && have; ++i) {
+        const int slot = i & 1, t = walk.t;
+        // the next tile's loads are in flight while this one waits for its slot
+        have = walk.next();
+        if (have) load(walk.t, next_l);
+        if (i >= 2) ok = mbar_wait(&sb.s_full[slot], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
+        if (ok && use_table && i >= 2) ok = mbar_wait(&sb.rng_empty[slot], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
+        if (!__all_sync(kFull, ok)) break;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k, row = t * p.npos + pos[k];
-        f.nl2[c] = -kLog2e * nl[k];
-        if (key0) f.sink[c] = sink[k];
-        if (walk.ranged(t)) f.rng[c] = row < r.q_len ? range_of(p.m, r, row) : make_int2(1, 0);
-        nl[k] = next_nl[k];
+        for (int k = 0; k < 4; ++k) {
+          // an infinite lse: a weight of zero (or, of -inf, infinity) whatever the score
+          const float v = fabsf(l[k]) == INFINITY ? copysignf(kHuge, -l[k]) : l[k] * inv;
+          const float hi = __bfloat162float(__float2bfloat16_rn(v));
+          const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
+          const uint32_t w0 = pack_bf16x2(hi, mid), w1 = pack_bf16x2((v - hi) - mid, 0.f);
+          *reinterpret_cast<uint4*>(sE + (1 + slot) * kExtBytes + ext_off(lane + 32 * k, 0)) = make_uint4(w0, w1, 0u, 0u);
+          l[k] = next_l[k];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_release(ext_bar + slot * 8);
+        if (use_table) {
+          if (walk.ranged(t))
+            for (int c = lane; c < kTile; c += 32) {
+              const int half = c / kCols, cc = c % kCols, row = (2 * t + half) * p.npos + cc / p.group;
+              sR[slot * kTile + c] = (cc < ncol && row < r.q_len) ? range_of(p.m, r, row) : make_int2(1, 0);
+            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.rng_full[slot]);
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sb.col_full[slot]);
     }
     if (!ok) sb.wc.abort = 1;
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- exponentials and sums
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const int row = quarter * 32 + lane, key = ja + row;
-    const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (kCols / 2);
+    const int row = quarter * 32 + lane;
+    const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
     const float sc = p.m.scale_log2;
     const uint64_t sc2 = f2_pack(sc, sc);
-    const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr && ja == 0;
-    long long p_lo, p_hi;
-    seen_by(p.m, key, p_lo, p_hi);
-    if (key > jb) p_hi = p_lo - 1;
-    // tiles all of whose rows see every key of the block: positions [in_lo, in_hi]
-    long long in_lo, in_hi, tmp;
-    seen_by(p.m, jb, in_lo, tmp);
-    seen_by(p.m, ja, tmp, in_hi);
-    if (jb >= p.m.first_tokens && ja < p.m.first_tokens) in_hi = min(in_hi, static_cast<long long>(p.m.first_tokens) + p.m.window_left);
-    uint64_t acc[2] = {0ull, 0ull};
+    const uint32_t s_empty0 = mapa_shared(smem_u32(&sb.s_empty[0]), 0);
+    float* w = p.partial != nullptr
+                   ? p.partial + ((static_cast<size_t>(split) * p.num_reqs + b) * p.hkv + h) * (static_cast<size_t>(p.n_kb) * kTile)
+                   : weight_row(p, b, h);
+    const bool add = p.partial == nullptr && p.accumulate;
     bool ok = true;
-    for (int i = 0; walk.next(); ++i) {
-      const int slot = i % kInfo;
-      ok = mbar_wait(&sb.col_full[slot], (i / kInfo) & 1, &sb.wc, p.err, kDevTimeoutOther);
-      if (ok) ok = mbar_wait(&sb.s_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
-      if (!ok) break;
-      tc_fence_after();
-      const ColInfo& f = sb.info[slot];
-      const int row0 = walk.t * p.npos;             // the tile's first row
-      const int valid = min(p.npos, r.q_len - row0);  // rows of the request in it
-      const long long p0 = static_cast<long long>(r.ctx) + row0;
-      const bool ranged = walk.ranged(walk.t);
-      const bool whole = valid == p.npos && p0 >= in_lo && p0 + valid - 1 <= in_hi && !ranged && !key0;
-      // columns of the tile that see this thread's key: [c_lo, c_hi]
-      const int c_lo = static_cast<int>(min(max(p_lo - p0, 0LL), static_cast<long long>(valid))) * p.group;
-      const int c_hi = static_cast<int>(min(max(p_hi - p0 + 1, 0LL), static_cast<long long>(valid))) * p.group - 1;
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t s[32];
-        tmem_ld_32x32b_x32(base + (i & 1) * kCols + cc * 32, s);
-        tmem_ld_wait(s);
-        if (cc == 1) {  // the scores are in registers: the buffer is free
+    int i = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      TileWalk walk = walk_of(p, r, kb, split, bits, false);
+      const int ja = walk.ja + rank * kKeys, jb = min(ja + kKeys - 1, walk.jb), key = ja + row;  // this CTA's keys
+      const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr && ja == 0;
+      long long p_lo, p_hi;
+      seen_by(p.m, key, p_lo, p_hi);
+      if (key > jb) p_hi = p_lo - 1;
+      // rows at positions [in_lo, in_hi] see every key of the block
+      long long in_lo, in_hi, tmp;
+      seen_by(p.m, jb, in_lo, tmp);
+      seen_by(p.m, ja, tmp, in_hi);
+      if (jb >= p.m.first_tokens && ja < p.m.first_tokens)
+        in_hi = min(in_hi, static_cast<long long>(p.m.first_tokens) + p.m.window_left);
+      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+      for (; ok && walk.next(); ++i) {
+        ok = mbar_wait(&sb.s_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
+        if (ok && use_table) ok = mbar_wait(&sb.rng_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
+        if (!ok) break;
+        tc_fence_after();
+        const int row0 = (2 * walk.t + half) * p.npos;          // this half's first row
+        const int valid = max(0, min(p.npos, r.q_len - row0));  // rows of the request in it
+        const long long p0 = static_cast<long long>(r.ctx) + row0;
+        const bool ranged = walk.ranged(walk.t);
+        const bool whole = valid == p.npos && p0 >= in_lo && p0 + valid - 1 <= in_hi && !ranged && !key0;
+        const uint32_t col = base + (i & 1) * kTile;
+        auto release = [&]() {  // the scores are in registers: the buffer is free
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sb.s_empty[i & 1]);
-        }
-        const int col0 = half * (kCols / 2) + cc * 32;
+          if (lane == 0) mbar_arrive_cluster(s_empty0 + (i & 1) * 8);
+        };
         if (whole) {
+          uint32_t s[2][32];
+          tmem_ld_32x32b_x32(col, s[0]);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 nl = *reinterpret_cast<const float4*>(&f.nl2[col0 + 4 * q]);
-            float a0, a1, a2, a3;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])), sc2, f2_pack(nl.x, nl.y)), a0, a1);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])), sc2, f2_pack(nl.z, nl.w)), a2, a3);
-            acc[0] = f2_add(acc[0], f2_pack(ex2_approx(a0), ex2_approx(a1)));
-            acc[1] = f2_add(acc[1], f2_pack(ex2_approx(a2), ex2_approx(a3)));
+          for (int cc = 0; cc < 4; ++cc) {
+            tmem_ld_wait(s[cc & 1]);
+            if (cc < 3) tmem_ld_32x32b_x32(col + 32 * (cc + 1), s[(cc + 1) & 1]);
+            else release();
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              float a0, a1;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(s[cc & 1][2 * q]), __uint_as_float(s[cc & 1][2 * q + 1])), sc2), a0, a1);
+              acc[q & 3] = f2_add(acc[q & 3], f2_pack(ex2_approx(a0), ex2_approx(a1)));
+            }
           }
         } else {
-          uint32_t bits = interval_bits(c_lo, c_hi, col0);
-          if (ranged && key <= jb) {
+          // columns of the half that see this thread's key: [c_lo, c_hi]
+          const int c_lo = static_cast<int>(min(max(p_lo - p0, 0LL), static_cast<long long>(valid))) * p.group;
+          const int c_hi = static_cast<int>(min(max(p_hi - p0 + 1, 0LL), static_cast<long long>(valid))) * p.group - 1;
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(col + 32 * cc, s);
+            uint32_t seen = interval_bits(c_lo, c_hi, 32 * cc);
+            if (ranged && key <= jb) {
 #pragma unroll 8
-            for (int q = 0; q < 32; ++q) {
-              const int2 e = f.rng[col0 + q];
-              bits |= static_cast<uint32_t>(key >= e.x && key <= e.y) << q;
+              for (int q = 0; q < 32; ++q) {
+                const int2 e = sR[(i & 1) * kTile + half * kCols + 32 * cc + q];
+                seen |= static_cast<uint32_t>(key >= e.x && key <= e.y) << q;
+              }
             }
-          }
-          if (bits != 0u) {
-            float sum = 0.f;
+            tmem_ld_wait(s);
+            if (cc == 3) release();
+            if (key0 && key == 0) {
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              float v = fmaf(__uint_as_float(s[q]), sc, f.nl2[col0 + q]);
-              if (key0 && key == 0) v += f.sink[col0 + q];
-              sum += ((bits >> q) & 1u) ? ex2_approx(v) : 0.f;
+              for (int q = 0; q < 32; ++q)
+                s[q] = __float_as_uint(__uint_as_float(s[q]) + sb.sink[32 * cc + q] / sc);
             }
-            acc[0] = f2_add(acc[0], f2_pack(sum, 0.f));
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float e0 = ex2_approx(__uint_as_float(s[2 * q]) * sc), e1 = ex2_approx(__uint_as_float(s[2 * q + 1]) * sc);
+              acc[q & 3] = f2_add(acc[q & 3], f2_pack((seen >> (2 * q)) & 1u ? e0 : 0.f, (seen >> (2 * q + 1)) & 1u ? e1 : 0.f));
+            }
           }
         }
+        if (use_table) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.rng_empty[i & 1]);
+        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sb.col_empty[slot]);
+      // a block's sums: the two halves of the columns
+      float x0, x1, x2, x3;
+      f2_unpack(f2_add(acc[0], acc[1]), x0, x1);
+      f2_unpack(f2_add(acc[2], acc[3]), x2, x3);
+      const float mine = (x0 + x1) + (x2 + x3);
+      if (half == 1) sb.part[row] = mine;
+      named_barrier(1, 256);
+      if (half == 0 && key <= jb && w != nullptr) {
+        const float total = mine + sb.part[row];
+        w[key] = add ? w[key] + total : total;
+      }
+      named_barrier(2, 256);  // (part is read before the next block's)
     }
     if (!ok) sb.wc.abort = 1;
-    float x0, x1, x2, x3;
-    f2_unpack(acc[0], x0, x1);
-    f2_unpack(acc[1], x2, x3);
-    const float mine = (x0 + x1) + (x2 + x3);
-    if (half == 1) sb.part[row] = mine;
-    named_barrier(1, 256);
-    if (half == 0 && key <= jb) {
-      const float total = mine + sb.part[row];
-      if (p.partial != nullptr) {
-        p.partial[((static_cast<size_t>(split) * p.num_reqs + b) * p.hkv + h) * (static_cast<size_t>(p.n_kb) * kKeys) + key] = total;
-      } else {
-        float* w = weight_row(p, b, h);
-        if (w != nullptr) w[key] = p.accumulate ? w[key] + total : total;
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // rank 0's MMAs and drain are complete
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 2 * kCols);
+  if (warp == 1) tmem_dealloc_pair(tmem, 2 * kTile);
 }
 
 // Adds the splits' partial sums up, in their order.
@@ -479,7 +590,7 @@ __global__ void __launch_bounds__(256) key_weights_combine_kernel(const KwParams
   if (p.skip_decode && r.q_len == 1) return;
   const int key = blockIdx.x * 256 + threadIdx.x;
   if (key >= r.k_len) return;
-  const size_t row = static_cast<size_t>(p.n_kb) * kKeys;
+  const size_t row = static_cast<size_t>(p.n_kb) * kTile;
   float total = 0.f;
   for (int s = 0; s < p.splits; ++s) total += p.partial[((static_cast<size_t>(s) * p.num_reqs + b) * p.hkv + h) * row + key];
   float* w = weight_row(p, b, h);
@@ -688,13 +799,24 @@ cudaError_t set_smem(K kern, int bytes, bool (&done)[64]) {
 }
 
 template <int NCH, bool PAGED>
-cudaError_t launch_prefill_rows(const KwParams& p, const CUtensorMap& mq, const CUtensorMap& mk, long long ctas,
+cudaError_t launch_prefill_rows(const KwParams& p, const CUtensorMap& mq, const CUtensorMap& mk, long long pairs,
                                 cudaStream_t stream) {
   static bool done[64] = {};
-  cudaError_t e = set_smem(key_weights_prefill_kernel<NCH, PAGED>, PfCfg<NCH>::SMEM, done);
+  cudaError_t e = set_smem(key_weights_prefill_kernel<NCH, PAGED>, pf_smem<NCH>(), done);
   if (e != cudaSuccess) return e;
-  key_weights_prefill_kernel<NCH, PAGED><<<static_cast<unsigned>(ctas), kPfThreads, PfCfg<NCH>::SMEM, stream>>>(mq, mk, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kPfThreads);
+  cfg.dynamicSmemBytes = pf_smem<NCH>();
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, key_weights_prefill_kernel<NCH, PAGED>, mq, mk, p);
 }
 
 template <int NCH, bool PAGED>
@@ -712,13 +834,13 @@ cudaError_t launch_decode_rows(const KwParams& p, int reqs, const CUtensorMap& m
   return cudaGetLastError();
 }
 
-// Parts the query tiles of a key block are shared by: enough CTAs for two
-// rounds, not fewer than eight tiles each.
+// Parts the query tiles of a key block are shared by: enough CTA pairs for two
+// rounds, not fewer than four tiles each.
 int split_count(int num_reqs, int hkv, int max_q_len, int max_k_len, int npos, int num_sms) {
-  const long long blocks = static_cast<long long>(num_reqs) * hkv * ((max_k_len + kKeys - 1) / kKeys);
-  const int tiles = (max_q_len + npos - 1) / npos;
+  const long long blocks = static_cast<long long>(num_reqs) * hkv * ((max_k_len + kTile - 1) / kTile);
+  const int tiles = (max_q_len + 2 * npos - 1) / (2 * npos);
   int s = 1;
-  while (s < 16 && blocks * s < 2LL * num_sms && tiles / (2 * s) >= 8) s *= 2;
+  while (s < 16 && blocks * s < num_sms && tiles / (2 * s) >= 4) s *= 2;
   return s;
 }
 
@@ -740,6 +862,7 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
   if ((causal != 0 && causal != 1) || (accumulate != 0 && accumulate != 1)) return MVP_ERR_ARG;
   if (num_decode_reqs < -1 || num_decode_reqs > num_reqs) return MVP_ERR_ARG;
   if (!(scale > 0.f) || scale > 3.0e38f) return MVP_ERR_ARG;  // NaN, <= 0, inf
+  if (scale < 1e-30f) return MVP_ERR_UNSUPPORTED;              // lse / scale stays finite
   if (max_q_len < 0 || max_k_len < 0 || num_slots < 0) return MVP_ERR_ARG;
   if (weight_stride < max_k_len || (slots == nullptr && num_slots < num_reqs)) return MVP_ERR_ARG;
   if (total_q == 0 && accumulate) return MVP_OK;  // nothing to add
@@ -804,20 +927,26 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
     KwParams pp = p;
     pp.req_offset = first;
     pp.skip_decode = 1;
-    pp.n_kb = (max_k_len + kKeys - 1) / kKeys;
+    pp.n_kb = (max_k_len + kTile - 1) / kTile;
     pp.splits = split_count(num_reqs - first, p.hkv, max_q_len, max_k_len, p.npos, num_sms);
-    const size_t one = static_cast<size_t>(num_reqs) * p.hkv * pp.n_kb * kKeys * sizeof(float);
+    const size_t one = static_cast<size_t>(num_reqs) * p.hkv * pp.n_kb * kTile * sizeof(float);
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) pp.splits = 1;
     while (pp.splits > 1 && one * pp.splits > workspace_bytes) pp.splits /= 2;
     pp.partial = pp.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-    const long long ctas = static_cast<long long>(pp.n_kb) * pp.splits * p.hkv * (num_reqs - first);
-    if (ctas > INT_MAX) return MVP_ERR_UNSUPPORTED;
+    // Key blocks per CTA pair: as many as leave four rounds of pairs (the next
+    // block's K loads behind this one's tiles; the pair's set-up is paid once).
+    // With a range table one, whose tiles are listed at the start.
+    const long long blocks = static_cast<long long>(pp.n_kb) * pp.splits * p.hkv * (num_reqs - first);
+    pp.blocks = 1;
+    if (range_table == nullptr) pp.blocks = static_cast<int>(std::max(1LL, std::min(8LL, blocks / (2LL * num_sms))));
+    const long long pairs = static_cast<long long>((pp.n_kb + pp.blocks - 1) / pp.blocks) * pp.splits * p.hkv * (num_reqs - first);
+    if (2 * pairs > INT_MAX) return MVP_ERR_UNSUPPORTED;
     cudaError_t e = cudaErrorInvalidValue;
     switch (head_dim) {
-      case 64: e = paged ? launch_prefill_rows<1, true>(pp, mq, mk, ctas, st) : launch_prefill_rows<1, false>(pp, mq, mk, ctas, st); break;
-      case 128: e = paged ? launch_prefill_rows<2, true>(pp, mq, mk, ctas, st) : launch_prefill_rows<2, false>(pp, mq, mk, ctas, st); break;
-      case 256: e = paged ? launch_prefill_rows<4, true>(pp, mq, mk, ctas, st) : launch_prefill_rows<4, false>(pp, mq, mk, ctas, st); break;
-      case 512: e = paged ? launch_prefill_rows<8, true>(pp, mq, mk, ctas, st) : launch_prefill_rows<8, false>(pp, mq, mk, ctas, st); break;
+      case 64: e = paged ? launch_prefill_rows<1, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<1, false>(pp, mq, mk, pairs, st); break;
+      case 128: e = paged ? launch_prefill_rows<2, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<2, false>(pp, mq, mk, pairs, st); break;
+      case 256: e = paged ? launch_prefill_rows<4, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<4, false>(pp, mq, mk, pairs, st); break;
+      case 512: e = paged ? launch_prefill_rows<8, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<8, false>(pp, mq, mk, pairs, st); break;
     }
     if (e != cudaSuccess) return MVP_ERR_CUDA;
     ++launches;
@@ -860,7 +989,7 @@ size_t mvp_key_weights_workspace_size(int num_reqs, int num_heads_kv, int max_q_
   // the most splits any group size and GPU of up to 160 SMs asks for
   const int s = max_q_len == 1 ? 1 : split_count(num_reqs, num_heads_kv, max_q_len, max_k_len, 1, 160);
   if (s < 2) return 0;
-  const size_t keys = (static_cast<size_t>(max_k_len) + kKeys - 1) / kKeys * kKeys;
+  const size_t keys = (static_cast<size_t>(max_k_len) + kTile - 1) / kTile * kTile;
   return static_cast<size_t>(s) * num_reqs * num_heads_kv * keys * sizeof(float);
 }
 

@@ -214,7 +214,7 @@ def test_key_weights_refusals(lib):
                      dict(scale=float("nan")), dict(stride=63), dict(slots_n=0), dict(max_k=0), dict(max_q=0),
                      dict(total_q=0, acc=0)):
             assert call(paged, **over) == mvp.MVP_ERR_ARG, over
-        for over in (dict(d=96), dict(hq=258), dict(q=A + 8), dict(k=A + 4), dict(table=A + 4)):
+        for over in (dict(d=96), dict(hq=258), dict(scale=1e-31), dict(q=A + 8), dict(k=A + 4), dict(table=A + 4)):
             assert call(paged, **over) == mvp.MVP_ERR_UNSUPPORTED, over
         assert call(paged, total_q=0) == mvp.MVP_OK
     for over in (dict(block=8), dict(block=24), dict(blocks=0), dict(max_blocks=3)):
