@@ -171,7 +171,7 @@ def test_evict_refusals(lib):
         assert call(**over) == mvp.MVP_ERR_UNSUPPORTED, over
     assert call(wsb=256) == mvp.MVP_ERR_CAPACITY
     assert call(reqs=0) == mvp.MVP_OK
-    assert mvp.kv_evict_workspace_size(2, 3, 65) == 256 + 2 * 3 * 3 * 4
+    assert mvp.kv_evict_workspace_size(2, 3, 65) == 256 + 2 * 3 * 5 * 4
     assert mvp.kv_evict_workspace_size(0, 3, 65) == 0
 
 
