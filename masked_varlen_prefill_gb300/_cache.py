@@ -14,14 +14,20 @@ import ctypes
 import numpy as np
 import torch
 
-from ._lib import MVP_OK, MvpError, load_library
+from ._lib import MVP_OK, MvpError, _on, _stream, load_library
 
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 
 
-def _need(dev, dtype, **tensors):
-    """Every tensor given (not None) is contiguous, of ``dtype``, on ``dev``."""
-    for name, t in tensors.items():
+def _need(dev, dtype, *named):
+    """name, tensor, name, tensor, ...: every tensor given (not None) is
+    contiguous, of ``dtype``, on ``dev``."""
+    for t in named[1::2]:
+        if t is not None and not (t.dtype is dtype and t.device == dev and t.is_contiguous()):
+            break
+    else:
+        return
+    for name, t in zip(named[::2], named[1::2]):
         if t is None:
             continue
         if t.device != dev:
@@ -45,28 +51,25 @@ def _p(t):
 def _call(fn_name, dev, stream, *args):
     """The C call with ``dev`` current (its tensors' device) on ``stream`` or
     the device's current stream; raises on a non-zero status."""
-    fn = getattr(load_library(), fn_name)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+    st = _on(dev, getattr(load_library(), fn_name), (*args, _stream(stream, dev)))
     if st != MVP_OK:
         raise MvpError(fn_name, st)
 
 
 def _caches(k_cache, v_cache, block_size):
     """The caches as [rows, Hkv, D] and their number of blocks."""
-    if k_cache.dim() == 4:
-        k_cache = k_cache.reshape(-1, k_cache.shape[2], k_cache.shape[3])
-        v_cache = v_cache.reshape(-1, v_cache.shape[2], v_cache.shape[3])
-    if k_cache.dim() != 3 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        raise ValueError("the caches differ in shape")
+    if len(shape) == 4:
+        k_cache = k_cache.reshape(-1, *shape[2:])
+        v_cache = v_cache.reshape(-1, *shape[2:])
+        shape = k_cache.shape
+    if len(shape) != 3:
         raise ValueError("the caches must be [num_blocks * block_size, Hkv, D]")
-    if block_size < 1 or k_cache.shape[0] % block_size != 0:
+    if block_size < 1 or shape[0] % block_size != 0:
         raise ValueError("cache rows must be a multiple of block_size")
-    return k_cache, v_cache, k_cache.shape[0] // block_size
+    return k_cache, v_cache, shape[0] // block_size
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -102,13 +105,16 @@ def rope_table(inv_freq, axes=None, num_axes=None, device=None) -> RopeTable:
 
 
 def _rows_of(name, t, dtype, dev):
-    """Row stride of a [total_q, heads, D] tensor whose heads are contiguous."""
-    if t.dim() != 3 or t.device != dev or t.dtype != dtype:
+    """Shape and row stride of a [total_q, heads, D] tensor whose heads are
+    contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or t.device != dev or t.dtype is not dtype:
         raise ValueError(f"{name} must be a {dtype} tensor [total_q, heads, D] on {dev}")
-    rows, heads, d = t.shape
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    row, head, one = t.stride()
+    rows, heads, d = shape
+    if one != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name}'s heads must be contiguous")
-    return t.stride(0) if rows > 1 else max(t.stride(0), heads * d)
+    return shape, row if rows > 1 else max(row, heads * d)
 
 
 def rope_append_paged(q, k, v, q_out, k_cache, v_cache, positions, table, cu_seqlens_q, seq_lens_k, block_table,
@@ -123,27 +129,29 @@ def rope_append_paged(q, k, v, q_out, k_cache, v_cache, positions, table, cu_seq
     """
     dev = _cuda_device(q_out, "q_out")
     dtype = q.dtype
-    if dtype != _BF16 and dtype != _F32:
+    if dtype is not _BF16 and dtype is not _F32:
         raise ValueError(f"q must be bfloat16 or float32, got {dtype}")
-    qs, ks, vs = _rows_of("q", q, dtype, dev), _rows_of("k", k, dtype, dev), _rows_of("v", v, dtype, dev)
+    q_shape, qs = _rows_of("q", q, dtype, dev)
+    k_shape, ks = _rows_of("k", k, dtype, dev)
+    v_shape, vs = _rows_of("v", v, dtype, dev)
     k_cache, v_cache, num_blocks = _caches(k_cache, v_cache, block_size)
-    _need(dev, _BF16, q_out=q_out, k_cache=k_cache, v_cache=v_cache)
-    _need(dev, _I32, positions=positions, table=table.entries, cu_seqlens_q=cu_seqlens_q, seq_lens_k=seq_lens_k,
-          block_table=block_table)
-    total, hq, d = q.shape
-    hkv = k_cache.shape[1]
-    if q_out.shape != q.shape or k.shape != (total, hkv, d) or v.shape != k.shape or k_cache.shape[2] != d:
+    _need(dev, _BF16, "q_out", q_out, "k_cache", k_cache, "v_cache", v_cache)
+    _need(dev, _I32, "positions", positions, "table", table.entries, "cu_seqlens_q", cu_seqlens_q, "seq_lens_k",
+          seq_lens_k, "block_table", block_table)
+    total, hq, d = q_shape
+    _, hkv, dk = k_cache.shape
+    if q_out.shape != q_shape or k_shape != (total, hkv, d) or v_shape != k_shape or dk != d:
         raise ValueError("q and q_out must be [total_q, Hq, D], k and v [total_q, Hkv, D], the caches [.., Hkv, D]")
     if positions.shape != (table.num_axes, total):
         raise ValueError(f"positions must be [{table.num_axes}, total_q]")
     num_reqs = seq_lens_k.shape[0]
-    if cu_seqlens_q.shape != (num_reqs + 1,) or block_table.dim() != 2 or block_table.shape[0] != num_reqs:
+    bt_shape = block_table.shape
+    if cu_seqlens_q.shape != (num_reqs + 1,) or len(bt_shape) != 2 or bt_shape[0] != num_reqs:
         raise ValueError("cu_seqlens_q must be [B + 1], seq_lens_k [B] and block_table [B, max_blocks_per_seq]")
-    _call("mvp_rope_append_paged", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype == _F32,
+    _call("mvp_rope_append_paged", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype is _F32,
           q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), positions.data_ptr(), table.entries.data_ptr(),
           table.num_axes, table.rot_dim, bool(adjacent), cu_seqlens_q.data_ptr(), seq_lens_k.data_ptr(),
-          block_table.data_ptr(), block_size, block_table.shape[1], num_blocks, num_reqs, total, hq, hkv, d, qs, ks,
-          vs)
+          block_table.data_ptr(), block_size, bt_shape[1], num_blocks, num_reqs, total, hq, hkv, d, qs, ks, vs)
 
 
 # ------------------------------------------------------------------ weights
@@ -155,10 +163,10 @@ def _key_weights(fn_name, q, k, lse, weights, slots, accumulate, cu_seqlens_q, k
                  max_k_len, total_k, num_decode_reqs, range_table, range_covered, causal, window_left, window_right,
                  first_tokens, sinks, sink_mode, scale, workspace, stream):
     dev = _cuda_device(q, "q")
-    _need(dev, _BF16, q=q, k=k)
-    _need(dev, _F32, lse=lse, sinks=sinks)
-    _need(dev, _I32, cu_seqlens_q=cu_seqlens_q, context_lens=context_lens, range_table=range_table,
-          range_covered=range_covered)
+    _need(dev, _BF16, "q", q, "k", k)
+    _need(dev, _F32, "lse", lse, "sinks", sinks)
+    _need(dev, _I32, "cu_seqlens_q", cu_seqlens_q, "context_lens", context_lens, "range_table", range_table,
+          "range_covered", range_covered)
     if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2]:
         raise ValueError("q must be [total_q, Hq, D] and the keys [.., Hkv, D]")
     total_q, hq, d = q.shape
@@ -175,7 +183,7 @@ def _key_weights(fn_name, q, k, lse, weights, slots, accumulate, cu_seqlens_q, k
     _weight_args(weights, slots, num_reqs, hkv, dev)
     ws = 0
     if workspace is not None:
-        _need(dev, torch.uint8, workspace=workspace)
+        _need(dev, torch.uint8, "workspace", workspace)
         ws = workspace.numel()
     rows = (total_q,) if total_k is None else (total_q, total_k)
     _call(fn_name, dev, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(), weights.data_ptr(), weights.shape[0],
@@ -194,7 +202,7 @@ def attn_key_weights_varlen(q, k, lse, weights, cu_seqlens_q, cu_seqlens_k, max_
     sums of the probabilities of the ``attn_fwd_varlen`` call with these
     arguments that wrote ``lse`` (see ``mvp_attn_key_weights_varlen``)."""
     dev = _cuda_device(q, "q")
-    _need(dev, _I32, cu_seqlens_k=cu_seqlens_k)
+    _need(dev, _I32, "cu_seqlens_k", cu_seqlens_k)
     if cu_seqlens_k.shape != cu_seqlens_q.shape:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must be [B + 1]")
     _key_weights("mvp_attn_key_weights_varlen", q, k, lse, weights, slots, accumulate, cu_seqlens_q,
@@ -211,7 +219,7 @@ def attn_key_weights_paged(q, k_cache, lse, weights, cu_seqlens_q, seq_lens_k, b
     ``attn_fwd_paged`` call with these arguments."""
     dev = _cuda_device(q, "q")
     k_cache, _, num_blocks = _caches(k_cache, k_cache, block_size)
-    _need(dev, _I32, seq_lens_k=seq_lens_k, block_table=block_table)
+    _need(dev, _I32, "seq_lens_k", seq_lens_k, "block_table", block_table)
     num_reqs = seq_lens_k.shape[0]
     if cu_seqlens_q.shape != (num_reqs + 1,) or block_table.dim() != 2 or block_table.shape[0] != num_reqs:
         raise ValueError("cu_seqlens_q must be [B + 1], seq_lens_k [B] and block_table [B, max_blocks_per_seq]")
@@ -227,11 +235,11 @@ def kv_evict_workspace_size(num_reqs, num_heads_kv, budget) -> int:
 
 
 def _weight_args(weights, slots, num_reqs, hkv, dev, name="weights"):
-    _need(dev, _F32, **{name: weights})
+    _need(dev, _F32, name, weights)
     if weights.dim() != 3 or weights.shape[1] != hkv:
         raise ValueError(f"{name} must be [num_slots, Hkv, max_len]")
     if slots is not None:
-        _need(dev, _I32, slots=slots)
+        _need(dev, _I32, "slots", slots)
         if slots.shape != (num_reqs,):
             raise ValueError("slots must be [B]")
 
@@ -250,14 +258,14 @@ def kv_evict_paged(k_cache, v_cache, weights, seq_lens_k, block_table, block_siz
     """
     dev = _cuda_device(k_cache, "k_cache")
     k_cache, v_cache, num_blocks = _caches(k_cache, v_cache, block_size)
-    _need(dev, _BF16, k_cache=k_cache, v_cache=v_cache)
-    _need(dev, _I32, seq_lens_k=seq_lens_k, block_table=block_table, block_table_out=block_table_out,
-          new_seq_lens=new_seq_lens, kept=kept)
-    _need(dev, torch.uint8, workspace=workspace)
+    _need(dev, _BF16, "k_cache", k_cache, "v_cache", v_cache)
+    _need(dev, _I32, "seq_lens_k", seq_lens_k, "block_table", block_table, "block_table_out", block_table_out,
+          "new_seq_lens", new_seq_lens, "kept", kept)
+    _need(dev, torch.uint8, "workspace", workspace)
     num_reqs, hkv, d = seq_lens_k.shape[0], k_cache.shape[1], k_cache.shape[2]
     _weight_args(weights, slots, num_reqs, hkv, dev)
     if weights_out is not None:
-        _need(dev, _F32, weights_out=weights_out)
+        _need(dev, _F32, "weights_out", weights_out)
         if weights_out.shape != weights.shape:
             raise ValueError("weights_out must be like weights")
     for t in (block_table, block_table_out):

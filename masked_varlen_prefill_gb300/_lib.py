@@ -165,18 +165,31 @@ class bounds_checked:
         return False
 
 
+# (Pointers go to ctypes as plain integers, and the current stream is read
+# without building a Stream object: on small batches a caller waits for this
+# host work.)
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+        if device.index is None:
+            return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
+
+
+def _on(dev, fn, args):
+    """fn(*args) with ``dev`` the current device."""
+    if dev.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _check_cuda(name, t, dtype, device):
-    if t is None:
+    if t is None or (t.is_cuda and t.dtype is dtype and t.device == device and t.is_contiguous()):
         return
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
@@ -258,9 +271,9 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
         if not plain:
             raise ValueError("first_tokens does not combine with variant, wait_limit_us, fault or mixed_prefill_sms")
         args.insert(22, int(first_tokens))
-        name, st = "mvp_attn_fwd_varlen_first", lib.mvp_attn_fwd_varlen_first(*args)
+        name, st = "mvp_attn_fwd_varlen_first", _on(dev, lib.mvp_attn_fwd_varlen_first, args)
     elif plain:
-        name, st = "mvp_attn_fwd_varlen", lib.mvp_attn_fwd_varlen(*args)
+        name, st = "mvp_attn_fwd_varlen", _on(dev, lib.mvp_attn_fwd_varlen, args)
     else:
         opts = AttnOptions(int(variant), int(wait_limit_us), int(fault), int(mixed_prefill_sms))
         name, st = "mvp_attn_fwd_varlen_ext", lib.mvp_attn_fwd_varlen_ext(*args, ctypes.byref(opts))
@@ -349,9 +362,9 @@ def attn_fwd_paged(q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_tab
             _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes, _stream(stream, dev)]
     if first_tokens != 0:
         args.insert(25, int(first_tokens))
-        name, st = "mvp_attn_fwd_paged_first", lib.mvp_attn_fwd_paged_first(*args)
+        name, st = "mvp_attn_fwd_paged_first", _on(dev, lib.mvp_attn_fwd_paged_first, args)
     else:
-        name, st = "mvp_attn_fwd_paged", lib.mvp_attn_fwd_paged(*args)
+        name, st = "mvp_attn_fwd_paged", _on(dev, lib.mvp_attn_fwd_paged, args)
     if st != MVP_OK:
         raise MvpError(name, st)
 

@@ -913,7 +913,11 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
   p.max_k_len = max_k_len;
   p.err = err;
 
-  const int decode_count = num_decode_reqs < 0 ? num_reqs : num_decode_reqs;
+  // Mixed in any order, but so many rows that every request has more than one
+  // (unless rows are padding): the prefill kernel takes them all, right for
+  // single tokens too, and the other one is not launched.
+  const bool no_single = num_decode_reqs < 0 && total_q > static_cast<long long>(num_reqs - 1) * max_q_len + 1;
+  const int decode_count = no_single ? 0 : (num_decode_reqs < 0 ? num_reqs : num_decode_reqs);
   const int first = num_decode_reqs < 0 ? 0 : num_decode_reqs;
   // Requests without queries (q_len 0) are set to 0 by the prefill kernel.
   const bool run_prefill = first < num_reqs && (max_q_len > 1 || !accumulate);
@@ -926,7 +930,7 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
     if (!encode_bf16_3d(&mq, q, head_dim, num_heads_q, total_q, 64, p.group, p.npos, true)) return MVP_ERR_UNSUPPORTED;
     KwParams pp = p;
     pp.req_offset = first;
-    pp.skip_decode = 1;
+    pp.skip_decode = no_single ? 0 : 1;
     pp.n_kb = (max_k_len + kTile - 1) / kTile;
     pp.splits = split_count(num_reqs - first, p.hkv, max_q_len, max_k_len, p.npos, num_sms);
     const size_t one = static_cast<size_t>(num_reqs) * p.hkv * pp.n_kb * kTile * sizeof(float);
