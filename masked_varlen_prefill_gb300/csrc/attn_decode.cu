@@ -211,21 +211,44 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
       const int kbox = PAGED ? min(C::KT, 1 << p.m.block_shift) : C::KT;
       int issued = 0;
       bool ok = true;
+      // First key of tile t, and (paged) the cache rows of its runs, one per
+      // kbox keys: looked up a tile ahead, so that the block ids' latency is
+      // not in the way of a freed stage.
+      auto key_of = [&](int t) {
+        const int w0 = w_lo + t * C::KT;
+        return w0 < n_first ? w0 : w0 + skip;
+      };
+      constexpr int kRuns = PAGED ? C::KT / 16 : 1;
+      int next[kRuns];
+      auto look_up = [&](int t) {
+        if constexpr (PAGED) {
+          const int key0 = key_of(min(t, n_tiles - 1));
+#pragma unroll
+          for (int i = 0; i < kRuns; ++i)
+            if (i * kbox < C::KT) next[i] = kv_row(p.m, b, k0, k_len, key0 + i * kbox);
+        }
+      };
+      look_up(0);
       for (int t = 0; t < n_tiles; ++t) {
         const int s = t % C::STAGES;
+        int rows[kRuns];
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) rows[i] = next[i];
+        look_up(t + 1);
         if (t >= C::STAGES &&
             !mbar_wait(&sb.empty[s], ((t / C::STAGES) - 1) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
           ok = false;
           break;
         }
         mbar_arrive_expect_tx(&sb.full[s], 2 * C::TILE);
-        const int w0 = w_lo + t * C::KT;
-        const int key0 = w0 < n_first ? w0 : w0 + skip;
         uint8_t* ks = smem + s * 2 * C::TILE;
         uint8_t* vs = ks + C::TILE;
         // one box per run of keys inside one cache block (the whole tile when packed)
-        for (int r = 0; r < C::KT; r += kbox) {
-          const int row = PAGED ? kv_row(p.m, b, k0, k_len, key0 + r) : k0 + key0 + r;
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+          const int r = i * kbox;
+          if (r >= C::KT) break;
+          const int row = PAGED ? rows[i] : k0 + key_of(t) + r;
 #pragma unroll
           for (int x = 0; x < C::NBOX; ++x) {
             tma_load_3d(ks + x * (C::KT * C::BOX * 2) + r * (C::BOX * 2), &map_k, &sb.full[s], x * C::BOX, hkv, row);
