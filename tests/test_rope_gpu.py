@@ -174,3 +174,13 @@ def test_stream_graph_and_checked_build():
         assert mvp.get_last_device_error() == mvp.MVP_OK
     for r, a in zip(ref, dbg):
         assert torch.equal(r, a)
+
+
+@pytest.mark.parametrize("rows", [2500, 5003])
+@pytest.mark.parametrize("hq,hkv,d,rot", [(2, 1, 64, 16), (4, 1, 64, 64), (8, 2, 64, 32)])
+def test_several_tokens_per_cta(rows, hq, hkv, d, rot):
+    """Many small rows: a CTA takes several, of one request or of several, and
+    the last CTA fewer."""
+    c = _case([rows - 400, 1, 0, 399], [rows, 9, 3, 450], hq, hkv, d, rot, 2, 16, torch.bfloat16, rows % 2 == 1,
+              seed=rows + rot, pad=3)
+    _check(c, *_run(c))
