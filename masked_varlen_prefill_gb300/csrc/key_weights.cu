@@ -118,10 +118,17 @@ __device__ __forceinline__ int2 range_of(const MaskParams& m, const Req& r, int 
 }
 
 // ------------------------------------------------------------------ prefill rows
-constexpr int kPfThreads = 384;  // producer, MMA, column and idle warps, 8 epilogue warps
+// Epilogue warpgroups: each takes half of a tile's columns (four with a quarter
+// each measured 2-8 % slower: the work per tile that every warp repeats).
+constexpr int kEpi = 2;
+constexpr int kEpiCols = 2 * kCols / kEpi;
+constexpr int kPfThreads = 128 + 128 * kEpi;  // producer, MMA, column and idle warps, epilogue warps
 constexpr int kMaxTileBits = 4096;
 constexpr int kTile = 2 * kCols;           // columns of a pair's tile
-constexpr int kExtBytes = kCols * 32;      // 128 rows x 16 dims of bf16
+constexpr int kExtBytes = kCols * 16;      // 128 rows x 8 dims of bf16
+// Slots of a tile's -lse / scale: the column warps run up to four tiles ahead of
+// the MMAs.
+constexpr int kExt = 4;
 constexpr float kHuge = 3.0e38f;           // (a bf16 value near it stays finite)
 
 template <int NCH>
@@ -130,18 +137,18 @@ struct PfCfg {
   static constexpr int STAGES = NCH <= 2 ? 8 : 5;                // Q chunks in flight
   static constexpr int K_BYTES = NCH * kChunkBytes;
   static constexpr int Q_OFF = KBUF * K_BYTES;
-  static constexpr int EXT_OFF = Q_OFF + STAGES * kChunkBytes;   // ones, then two slots
-  static constexpr int RNG_OFF = EXT_OFF + 3 * kExtBytes;        // two slots of kTile intervals
+  static constexpr int EXT_OFF = Q_OFF + STAGES * kChunkBytes;   // ones, the slots, zeros
+  static constexpr int ZERO_OFF = EXT_OFF + (1 + kExt) * kExtBytes;
+  static constexpr int RNG_OFF = ZERO_OFF + kExtBytes;           // two slots of kTile intervals
   static constexpr int SHARED_OFF = RNG_OFF + 2 * kTile * 8;
 };
 
 struct __align__(16) PfShared {
   uint32_t range_bits[kMaxTileBits / 32];  // tiles with a row whose range meets this key block
-  float part[kKeys];                       // second epilogue warpgroup's sums
   float sink[kCols];                       // key-0 sinks of a CTA's columns, log2 units
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full[8], q_empty[8];
-  uint64_t ext_full[2];
+  uint64_t ext_full[kExt], ext_empty[kExt];
   uint64_t s_full[2], s_empty[2];
   uint64_t rng_full[2], rng_empty[2];
   uint64_t final_mma;
@@ -152,6 +159,7 @@ template <int NCH>
 constexpr int pf_smem() {
   return PfCfg<NCH>::SHARED_OFF + static_cast<int>(sizeof(PfShared)) + 1024;
 }
+static_assert((kEpi - 1) * kKeys * 4 <= 2 * kTile * 8, "the sums fit the range slots");
 static_assert(pf_smem<4>() <= 227 * 1024 && pf_smem<8>() <= 227 * 1024 && pf_smem<2>() <= 227 * 1024, "smem budget");
 
 // Key block of the pair, and the query tiles that see any of it: [t_lo, t_hi)
@@ -167,10 +175,13 @@ struct TileWalk {
   }
   __device__ __forceinline__ bool next() {  // t: the tile to visit
     ++t;
-    while (t < t_hi && t < t_lo && !ranged(t)) ++t;
+    if (bits != nullptr)
+      while (t < t_hi && t < t_lo && !ranged(t)) ++t;
     return t < t_hi;
   }
 };
+
+__device__ __forceinline__ long long floor_div(long long a, int b) { return a >= 0 ? a / b : -((-a + b - 1) / b); }
 
 // bits: the block's range bits, or null; whole: before the split.
 __device__ __forceinline__ TileWalk walk_of(const KwParams& p, const Req& r, int kb, int split, const uint32_t* bits,
@@ -202,13 +213,12 @@ __device__ __forceinline__ TileWalk walk_of(const KwParams& p, const Req& r, int
 }
 
 // Descriptor of an operand of 16 dims without swizzle: 8-row x 16-byte core
-// matrices, the two along K 128 bytes apart, the row groups 256.
-__device__ __forceinline__ uint64_t ext_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
-         (static_cast<uint64_t>(256 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+// matrices, the row groups of dims 0 .. 7 128 bytes apart, dims 8 .. 15 (zeros,
+// one block for all of them) `zeros` bytes behind.
+__device__ __forceinline__ uint64_t ext_desc(uint32_t saddr, int zeros) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(zeros >> 4) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
-// Byte offset of dims 8 * half .. + 7 of a row in it.
-__device__ __forceinline__ int ext_off(int row, int half) { return (row >> 3) * 256 + half * 128 + (row & 7) * 16; }
 
 template <int NCH, bool PAGED>
 __global__ void __launch_bounds__(kPfThreads, 1)
@@ -259,11 +269,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sb.k_full[i], 1);
       mbar_init(&sb.k_empty[i], 1);
-      mbar_init(&sb.ext_full[i], 2);   // both CTAs' column warps
       mbar_init(&sb.s_full[i], 1);
-      mbar_init(&sb.s_empty[i], 16);   // both CTAs' epilogue warps (rank 0's barrier)
+      mbar_init(&sb.s_empty[i], 8 * kEpi);  // both CTAs' epilogue warps (rank 0's barrier)
       mbar_init(&sb.rng_full[i], 1);
-      mbar_init(&sb.rng_empty[i], 8);
+      mbar_init(&sb.rng_empty[i], 4 * kEpi);
+    }
+    for (int i = 0; i < kExt; ++i) {
+      mbar_init(&sb.ext_full[i], 2);  // both CTAs' column warps
+      mbar_init(&sb.ext_empty[i], 1);
     }
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&sb.q_full[i], 1);
@@ -279,13 +292,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tmem_relinquish_pair();
   }
   // Operand parts that nothing else writes: ones in the first three dims of the
-  // keys' extension, zeros in dims 8 .. 15 of the columns', and zeros in the
-  // rows of a Q chunk past the last column.
+  // keys' extension, the zeros of dims 8 .. 15, and zeros in the rows of a Q
+  // chunk past the last column.
   for (int i = threadIdx.x; i < kCols; i += kPfThreads) {
-    *reinterpret_cast<uint4*>(sE + ext_off(i, 0)) = make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u);
-    *reinterpret_cast<uint4*>(sE + ext_off(i, 1)) = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(sE + kExtBytes + ext_off(i, 1)) = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(sE + 2 * kExtBytes + ext_off(i, 1)) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(sE + 16 * i) = make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u);
+    *reinterpret_cast<uint4*>(smem + C::ZERO_OFF + 16 * i) = make_uint4(0, 0, 0, 0);
     const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr && i < ncol;
     sb.sink[i] = key0 ? __ldg(p.m.sinks + h * p.group + i % p.group) * kLog2e : 0.f;
   }
@@ -359,7 +370,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     constexpr uint32_t idesc = idesc_bf16_f32(2 * kKeys, kTile, false, false);
     const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t ones = ext_desc(smem_u32(sE)), ext = ext_desc(smem_u32(sE + kExtBytes));
+    const uint64_t ones = ext_desc(smem_u32(sE), C::ZERO_OFF - C::EXT_OFF);
     const bool issuer = elect_one();
     bool ok = true;
     int n = 0, nb = 0, i = 0;  // chunks, K blocks, tiles
@@ -370,13 +381,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int ks = nb % C::KBUF;
         if (!any) ok = mbar_wait(&sb.k_full[ks], (nb / C::KBUF) & 1, &sb.wc, p.err, kDevTimeoutLoad);
         any = true;
-        if (ok && i >= 2) ok = mbar_wait_cluster(&sb.s_empty[i & 1], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutSoftmax);
-        if (ok) ok = mbar_wait_cluster(&sb.ext_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
+        const int es = i % kExt;
+        if (ok) ok = mbar_wait_spin(&sb.ext_full[es], (i / kExt) & 1, &sb.wc, p.err, kDevTimeoutOther);
+        if (ok && i >= 2) ok = mbar_wait_spin(&sb.s_empty[i & 1], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutSoftmax);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (i & 1) * kTile;
         const uint64_t dk = desc_add(dk0, static_cast<uint32_t>((ks * C::K_BYTES) >> 4));
-        if (issuer) mma_ss_one<2>(d, ones, desc_add(ext, static_cast<uint32_t>(((i & 1) * kExtBytes) >> 4)), idesc, 0u);
+        if (issuer)
+          mma_ss_one<2>(d, ones, ext_desc(smem_u32(sE + (1 + es) * kExtBytes), (kExt - es) * kExtBytes), idesc, 0u);
+        __syncwarp();
+        mma_commit_elect<2>(&sb.ext_empty[es]);
         for (int c = 0; c < NCH; ++c, ++n) {
           const int s = n % C::STAGES;
           if (!mbar_wait_spin(&sb.q_full[s], (n / C::STAGES) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
@@ -433,11 +448,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       bool have = walk.next();
       if (have) load(walk.t, l);
       for (; ok && have; ++i) {
-        const int slot = i & 1, t = walk.t;
+        const int slot = i & 1, es = i % kExt, t = walk.t;
         // the next tile's loads are in flight while this one waits for its slot
         have = walk.next();
         if (have) load(walk.t, next_l);
-        if (i >= 2) ok = mbar_wait(&sb.s_full[slot], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
+        if (i >= kExt) ok = mbar_wait(&sb.ext_empty[es], ((i / kExt) - 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
         if (ok && use_table && i >= 2) ok = mbar_wait(&sb.rng_empty[slot], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
         if (!__all_sync(kFull, ok)) break;
 #pragma unroll
@@ -447,12 +462,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const float hi = __bfloat162float(__float2bfloat16_rn(v));
           const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
           const uint32_t w0 = pack_bf16x2(hi, mid), w1 = pack_bf16x2((v - hi) - mid, 0.f);
-          *reinterpret_cast<uint4*>(sE + (1 + slot) * kExtBytes + ext_off(lane + 32 * k, 0)) = make_uint4(w0, w1, 0u, 0u);
+          *reinterpret_cast<uint4*>(sE + (1 + es) * kExtBytes + 16 * (lane + 32 * k)) = make_uint4(w0, w1, 0u, 0u);
           l[k] = next_l[k];
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_release(ext_bar + slot * 8);
+        // (released at CTA scope: what the arrival publishes are this CTA's own
+        // shared-memory writes, made visible to the tensor core by the fence
+        // above; a release at cluster scope also waits for the loads in flight,
+        // and took a tile from 1150 to 1300 ns)
+        if (lane == 0) mbar_arrive_cluster(ext_bar + es * 8);
         if (use_table) {
           if (walk.ranged(t))
             for (int c = lane; c < kTile; c += 32) {
@@ -467,9 +486,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (!ok) sb.wc.abort = 1;
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- exponentials and sums
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int quarter = warp & 3, part = (warp - 4) >> 2;
+    const int half = part / (kEpi / 2), col0 = (part % (kEpi / 2)) * kEpiCols;  // of a half's columns: [col0, col0 + kEpiCols)
     const int row = quarter * 32 + lane;
-    const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kCols;
+    const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * kEpiCols;
     const float sc = p.m.scale_log2;
     const uint64_t sc2 = f2_pack(sc, sc);
     const uint32_t s_empty0 = mapa_shared(smem_u32(&sb.s_empty[0]), 0);
@@ -492,30 +512,35 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       seen_by(p.m, ja, tmp, in_hi);
       if (jb >= p.m.first_tokens && ja < p.m.first_tokens)
         in_hi = min(in_hi, static_cast<long long>(p.m.first_tokens) + p.m.window_left);
+      // ... that is, the tiles [w_lo, w_hi] whose npos rows of this half all do
+      // (64-bit divisions, once per block: done per tile they and the walk took
+      // 700 of 2200 clocks a tile).
+      const int rows2 = 2 * p.npos;
+      const long long at0 = static_cast<long long>(r.ctx) + half * p.npos;  // position of tile 0's first row of the half
+      const int w_lo = static_cast<int>(max(0LL, min(-floor_div(at0 - in_lo, rows2), 1LL << 30)));
+      int w_hi = static_cast<int>(max(-1LL, min(floor_div(in_hi - at0 - p.npos + 1, rows2),
+                                                floor_div(r.q_len - p.npos - half * p.npos, rows2))));
+      if (key0) w_hi = -1;
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-      for (; ok && walk.next(); ++i) {
+      for (; walk.next(); ++i) {
         ok = mbar_wait(&sb.s_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
         if (ok && use_table) ok = mbar_wait(&sb.rng_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
         if (!ok) break;
         tc_fence_after();
-        const int row0 = (2 * walk.t + half) * p.npos;          // this half's first row
-        const int valid = max(0, min(p.npos, r.q_len - row0));  // rows of the request in it
-        const long long p0 = static_cast<long long>(r.ctx) + row0;
-        const bool ranged = walk.ranged(walk.t);
-        const bool whole = valid == p.npos && p0 >= in_lo && p0 + valid - 1 <= in_hi && !ranged && !key0;
         const uint32_t col = base + (i & 1) * kTile;
         auto release = [&]() {  // the scores are in registers: the buffer is free
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(s_empty0 + (i & 1) * 8);
         };
-        if (whole) {
+        const bool ranged = walk.ranged(walk.t);
+        if (walk.t >= w_lo && walk.t <= w_hi && !ranged) {
           uint32_t s[2][32];
           tmem_ld_32x32b_x32(col, s[0]);
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
+          for (int cc = 0; cc < kEpiCols / 32; ++cc) {
             tmem_ld_wait(s[cc & 1]);
-            if (cc < 3) tmem_ld_32x32b_x32(col + 32 * (cc + 1), s[(cc + 1) & 1]);
+            if (cc < kEpiCols / 32 - 1) tmem_ld_32x32b_x32(col + 32 * (cc + 1), s[(cc + 1) & 1]);
             else release();
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
@@ -525,27 +550,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
           }
         } else {
+          const int row0 = (2 * walk.t + half) * p.npos;          // this half's first row
+          const int valid = max(0, min(p.npos, r.q_len - row0));  // rows of the request in it
+          const long long p0 = static_cast<long long>(r.ctx) + row0;
           // columns of the half that see this thread's key: [c_lo, c_hi]
           const int c_lo = static_cast<int>(min(max(p_lo - p0, 0LL), static_cast<long long>(valid))) * p.group;
           const int c_hi = static_cast<int>(min(max(p_hi - p0 + 1, 0LL), static_cast<long long>(valid))) * p.group - 1;
 #pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
+          for (int cc = 0; cc < kEpiCols / 32; ++cc) {
             uint32_t s[32];
             tmem_ld_32x32b_x32(col + 32 * cc, s);
-            uint32_t seen = interval_bits(c_lo, c_hi, 32 * cc);
+            uint32_t seen = interval_bits(c_lo, c_hi, col0 + 32 * cc);
             if (ranged && key <= jb) {
 #pragma unroll 8
               for (int q = 0; q < 32; ++q) {
-                const int2 e = sR[(i & 1) * kTile + half * kCols + 32 * cc + q];
+                const int2 e = sR[(i & 1) * kTile + part * kEpiCols + 32 * cc + q];
                 seen |= static_cast<uint32_t>(key >= e.x && key <= e.y) << q;
               }
             }
             tmem_ld_wait(s);
-            if (cc == 3) release();
+            if (cc == kEpiCols / 32 - 1) release();
             if (key0 && key == 0) {
 #pragma unroll
               for (int q = 0; q < 32; ++q)
-                s[q] = __float_as_uint(__uint_as_float(s[q]) + sb.sink[32 * cc + q] / sc);
+                s[q] = __float_as_uint(__uint_as_float(s[q]) + sb.sink[col0 + 32 * cc + q] / sc);
             }
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
@@ -559,18 +587,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (lane == 0) mbar_arrive(&sb.rng_empty[i & 1]);
         }
       }
-      // a block's sums: the two halves of the columns
+      // a block's sums: the warpgroups' parts of the columns, in their order
       float x0, x1, x2, x3;
       f2_unpack(f2_add(acc[0], acc[1]), x0, x1);
       f2_unpack(f2_add(acc[2], acc[3]), x2, x3);
-      const float mine = (x0 + x1) + (x2 + x3);
-      if (half == 1) sb.part[row] = mine;
-      named_barrier(1, 256);
-      if (half == 0 && key <= jb && w != nullptr) {
-        const float total = mine + sb.part[row];
+      float total = (x0 + x1) + (x2 + x3);
+      // (through the range intervals' slots, once every warp is done with those)
+      float* parts = reinterpret_cast<float*>(sR);  // [kEpi - 1][kKeys]
+      if (use_table) named_barrier(3, 128 * kEpi);
+      if (part > 0) parts[(part - 1) * kKeys + row] = total;
+      named_barrier(1, 128 * kEpi);
+      if (part == 0 && key <= jb && w != nullptr) {
+#pragma unroll
+        for (int e = 0; e < kEpi - 1; ++e) total += parts[e * kKeys + row];
         w[key] = add ? w[key] + total : total;
       }
-      named_barrier(2, 256);  // (part is read before the next block's)
+      named_barrier(2, 128 * kEpi);  // (they are read before the next block's)
     }
     if (!ok) sb.wc.abort = 1;
   }
