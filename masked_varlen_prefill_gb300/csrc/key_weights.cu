@@ -866,13 +866,16 @@ cudaError_t launch_decode_rows(const KwParams& p, int reqs, const CUtensorMap& m
   return cudaGetLastError();
 }
 
-// Parts the query tiles of a key block are shared by: enough CTA pairs for two
-// rounds, not fewer than four tiles each.
+// Parts the query tiles of a key block are shared by: while half of the GPU's CTA
+// pairs would have no block, not fewer than four tiles each.  Measured at D =
+// 256: one 2048-row prompt of 16/8 heads (64 blocks for 76 pairs) 27 us alone,
+// 31 in two parts, 40 in four (a pair's set-up, the second kernel); a 4096-row
+// prompt of 8/2 heads (32 blocks) 80 us alone, 47 in two, 49 in four.
 int split_count(int num_reqs, int hkv, int max_q_len, int max_k_len, int npos, int num_sms) {
   const long long blocks = static_cast<long long>(num_reqs) * hkv * ((max_k_len + kTile - 1) / kTile);
   const int tiles = (max_q_len + 2 * npos - 1) / (2 * npos);
   int s = 1;
-  while (s < 16 && blocks * s < num_sms && tiles / (2 * s) >= 4) s *= 2;
+  while (s < 16 && blocks * s < num_sms / 4 && tiles / (2 * s) >= 4) s *= 2;
   return s;
 }
 

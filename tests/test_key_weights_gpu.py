@@ -162,12 +162,12 @@ def test_explicit_contexts_and_rows_that_see_nothing():
     Case(w, 5, ctx=[-2, 5000, 700, -3]).check_all(16)
 
 
-@pytest.mark.parametrize("q,k", [([700], [700]), ([2000], [2000]), ([300], [9000])])
+@pytest.mark.parametrize("q,k", [([700], [700]), ([2000], [2000]), ([1500, 40], [2100, 300])])
 def test_rows_shared_by_splits(q, k):
     """Few key blocks: the workspace lets several CTAs share a block's rows."""
     w = _w(q, k, 16, 2, 64, seed=q[0])
     c = Case(w)
-    assert mvp.key_weights_workspace_size(1, 2, q[0], k[0]) > 0
+    assert mvp.key_weights_workspace_size(len(q), 2, q[0], k[0]) > 0
     a = c.check_all(64)
     b = c.run(ws=False)
     c.check(b)
