@@ -930,7 +930,7 @@ def run_gpu(args, world, rank, local):
         roofline = {"bound": "tensor", "achieved": achieved, "peak": peak_t, "unit": "TFLOP/s",
                     "frac": achieved / peak_t,
                     "traffic": (None if (args.paged or args.scaled or args.scan)
-                                else load_traffic(os.path.join(kernel_dir, "attn_prefill.cu"), args.workload)),
+                                else load_traffic(os.path.join(kernel_dir, "attn_prefill.cuh"), args.workload)),
                     "kernel": f"attn_prefill_kernel (D={w.head_dim})",
                     "peak_source": f"bf16_tflops (burst) of {peak_src}", "kernel_ms_per_launch": 1e3 * pre_s}
     else:

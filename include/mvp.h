@@ -308,7 +308,9 @@ int mvp_attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
  *   visible = base || rng || (j < first_tokens
  *                             && (causal ? j <= p : window_right < 0 || j <= p + window_right))
  * (tokens, not the per-head sink logits, which combine with them as with any
- * other mask).  first_tokens >= 0; 0, or window_left = -1, is the plain call
+ * other mask).  As in the plain calls, V of a masked key that shares a 128-key
+ * tile with a visible one must be finite (it is multiplied by a probability of
+ * zero); K of masked keys may hold anything.  first_tokens >= 0; 0, or window_left = -1, is the plain call
  * bit for bit.  The key tiles between the first tokens and the window are
  * never read.  All other arguments, results and errors are those of the plain
  * calls; MVP_ERR_ARG also for first_tokens < 0.
@@ -574,7 +576,7 @@ int mvp_attn_accounting(const int32_t* cu_seqlens_q, const int32_t* seq_lens_k, 
  * rot_dim       16 .. head_dim, a multiple of 16.  head_dim: 16 .. 512, a
  *               multiple of 8.
  * Rows at or past cu_seqlens_q[num_reqs] (a padded batch) are left as they
- * were, in q_out too.
+ * were, in q_out too.  No two rows may be keys of the same cache row.
  * Errors: MVP_ERR_ARG, MVP_ERR_UNSUPPORTED (head_dim, rot_dim, alignment),
  * MVP_ERR_CUDA.
  */
@@ -681,8 +683,8 @@ size_t mvp_key_weights_workspace_size(int num_reqs, int num_heads_kv, int max_q_
  *               the same time need separate workspaces.
  * Errors: MVP_ERR_ARG (also first_tokens + recent_tokens > budget, a table or
  * weight row too short, new_seq_lens == seq_lens_k), MVP_ERR_CAPACITY
- * (workspace too small), MVP_ERR_UNSUPPORTED (head_dim, alignment),
- * MVP_ERR_CUDA.  num_reqs == 0: nothing is done.
+ * (workspace too small), MVP_ERR_UNSUPPORTED (head_dim, alignment, budget or
+ * max_k_len above 2^30), MVP_ERR_CUDA.  num_reqs == 0: nothing is done.
  */
 int mvp_kv_evict_paged(void* k_cache, void* v_cache, const float* weights, float* weights_out, int num_slots,
                        long long weight_stride, const int32_t* slots, const int32_t* seq_lens_k,
@@ -705,9 +707,9 @@ int mvp_get_last_device_error(void* stream);
 /* Static string for a status code. */
 const char* mvp_status_str(int status);
 
-/* Number of kernel launches the last successful mvp_attn_fwd_varlen /
- * mvp_attn_fwd_paged / mvp_fill_query_ranges call enqueued on this thread
- * (for launch accounting). */
+/* Number of kernel launches the last successful mvp_attn_* /
+ * mvp_fill_query_ranges / mvp_rope_append_paged / mvp_kv_evict_paged call
+ * enqueued on this thread (for launch accounting). */
 int mvp_last_launch_count(void);
 
 #ifdef __cplusplus

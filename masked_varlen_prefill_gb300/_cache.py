@@ -128,6 +128,7 @@ def rope_append_paged(q, k, v, q_out, k_cache, v_cache, positions, table, cu_seq
     [num_axes, total_q]; table a ``RopeTable``.
     """
     dev = _cuda_device(q_out, "q_out")
+    block_size = int(block_size)
     dtype = q.dtype
     if dtype is not _BF16 and dtype is not _F32:
         raise ValueError(f"q must be bfloat16 or float32, got {dtype}")
@@ -186,11 +187,12 @@ def _key_weights(fn_name, q, k, lse, weights, slots, accumulate, cu_seqlens_q, k
         _need(dev, torch.uint8, "workspace", workspace)
         ws = workspace.numel()
     rows = (total_q,) if total_k is None else (total_q, total_k)
+    scale = d ** -0.5 if scale is None else float(scale)
     _call(fn_name, dev, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(), weights.data_ptr(), weights.shape[0],
           weights.shape[2], _p(slots), bool(accumulate), cu_seqlens_q.data_ptr(), *key_args, _p(context_lens),
-          num_reqs, *rows, max_q_len, max_k_len, num_decode_reqs, hq, hkv, d, _p(range_table), _p(range_covered),
-          bool(causal), window_left, window_right, first_tokens, _p(sinks), sink_mode,
-          d ** -0.5 if scale is None else scale, _p(workspace), ws)
+          num_reqs, *rows, int(max_q_len), int(max_k_len), int(num_decode_reqs), hq, hkv, d, _p(range_table),
+          _p(range_covered), bool(causal), int(window_left), int(window_right), int(first_tokens), _p(sinks),
+          int(sink_mode), scale, _p(workspace), ws)
 
 
 def attn_key_weights_varlen(q, k, lse, weights, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_len, *, slots=None,
@@ -218,6 +220,7 @@ def attn_key_weights_paged(q, k_cache, lse, weights, cu_seqlens_q, seq_lens_k, b
     """``attn_key_weights_varlen`` over a paged cache: the weights of the
     ``attn_fwd_paged`` call with these arguments."""
     dev = _cuda_device(q, "q")
+    block_size = int(block_size)
     k_cache, _, num_blocks = _caches(k_cache, k_cache, block_size)
     _need(dev, _I32, "seq_lens_k", seq_lens_k, "block_table", block_table)
     num_reqs = seq_lens_k.shape[0]
@@ -257,6 +260,7 @@ def kv_evict_paged(k_cache, v_cache, weights, seq_lens_k, block_table, block_siz
     ``block_table_out`` / ``weights_out`` say where the kept keys go.
     """
     dev = _cuda_device(k_cache, "k_cache")
+    block_size, budget = int(block_size), int(budget)
     k_cache, v_cache, num_blocks = _caches(k_cache, v_cache, block_size)
     _need(dev, _BF16, "k_cache", k_cache, "v_cache", v_cache)
     _need(dev, _I32, "seq_lens_k", seq_lens_k, "block_table", block_table, "block_table_out", block_table_out,
@@ -276,6 +280,6 @@ def kv_evict_paged(k_cache, v_cache, weights, seq_lens_k, block_table, block_siz
     _call("mvp_kv_evict_paged", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
           _p(weights_out), weights.shape[0], weights.shape[2], _p(slots), seq_lens_k.data_ptr(),
           block_table.data_ptr(), _p(block_table_out), block_size, block_table.shape[1],
-          0 if block_table_out is None else block_table_out.shape[1], num_blocks, num_reqs, max_k_len, hkv, d, budget,
-          first_tokens, recent_tokens, new_seq_lens.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
+          0 if block_table_out is None else block_table_out.shape[1], num_blocks, num_reqs, int(max_k_len), hkv, d, budget,
+          int(first_tokens), int(recent_tokens), new_seq_lens.data_ptr(), kept.data_ptr(), workspace.data_ptr(),
           workspace.numel())

@@ -505,6 +505,7 @@ int mvp_kv_evict_paged(void* k_cache, void* v_cache, const float* weights, float
   if (head_dim < 16 || head_dim > 512 || head_dim % 8 != 0) return MVP_ERR_UNSUPPORTED;
   if (budget < 1 || first_tokens < 0 || recent_tokens < 0) return MVP_ERR_ARG;
   if (static_cast<long long>(first_tokens) + recent_tokens > budget) return MVP_ERR_ARG;
+  if (budget > (1 << 30) || max_k_len > (1 << 30)) return MVP_ERR_UNSUPPORTED;  // indices stay in an int
   int shift = 0;
   while (shift < 30 && (1 << shift) < block_size) ++shift;
   if (block_size < 16 || block_size > 256 || (1 << shift) != block_size) return MVP_ERR_ARG;

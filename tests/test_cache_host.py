@@ -167,7 +167,7 @@ def test_evict_refusals(lib):
                  dict(max_blocks=6), dict(new=A), dict(stride=99), dict(slots_n=1), dict(bt_out=A, max_out=3),
                  dict(first=2 ** 31 - 1, recent=2 ** 31 - 1)):
         assert call(**over) == mvp.MVP_ERR_ARG, over
-    for over in (dict(d=8), dict(d=100), dict(d=520), dict(k=A + 8), dict(v=A + 2), dict(ws=A + 4)):
+    for over in (dict(d=8), dict(d=100), dict(d=520), dict(budget=(1 << 30) + 1), dict(k=A + 8), dict(v=A + 2), dict(ws=A + 4)):
         assert call(**over) == mvp.MVP_ERR_UNSUPPORTED, over
     assert call(wsb=256) == mvp.MVP_ERR_CAPACITY
     assert call(reqs=0) == mvp.MVP_OK

@@ -224,6 +224,56 @@ def test_streams_graph_and_checked_build():
         assert torch.equal(ref, out)
 
 
+def test_padded_batches():
+    """Rows past the last request (a batch padded to a capacity): with total_q
+    so large that every request could have several rows, single-token ones are
+    the prefill kernel's; whatever the rows hold, nothing changes."""
+    w = _w([1, 5, 0, 3], [300, 40, 17, 700], 4, 2, 64, 90, sink=1, seed=12)
+    c = Case(w, 3)
+    ref = c.run()
+    for pad in (1, 30):
+        q = torch.full((w.total_q + pad, 4, 64), float("nan"), dtype=torch.bfloat16, device=c.dev)
+        q[:w.total_q] = c.x[0]
+        lse = torch.full((4, w.total_q + pad), float("nan"), device=c.dev)
+        lse[:, :w.total_q] = torch.tensor(c.lse, device=c.dev)
+        out = torch.tensor(c.w0, device=c.dev)
+        mvp.attn_key_weights_varlen(q, c.x[1], lse, out, c.t32(c.cu_q), c.t32(c.cu_k), 5, c.max_k, window_left=90,
+                                    first_tokens=3, sinks=c.x[3], sink_mode=1, scale=w.scale)
+        c.check(out)
+        if pad == 1:
+            assert torch.equal(ref, out)
+
+
+def test_far_rows_of_a_large_cache():
+    """Cache rows past 2^32 bytes: the last blocks of a 5 GB cache."""
+    d, hkv, block = 128, 8, 256
+    blocks = 5 * (1 << 30) // (d * hkv * 2 * block)
+    kc = torch.zeros((blocks * block, hkv, d), dtype=torch.bfloat16, device="cuda")
+    w = _w([40, 1], [600, 500], 16, hkv, d, seed=13)
+    c = Case(w)
+    small, _, bt, sl = workloads.to_paged(c.x[1], c.x[2], w.k_lens, block, seed=3)
+    shift = blocks - small.shape[0] // block
+    kc[shift * block:] = small
+    out = torch.tensor(c.w0, device=c.dev)
+    bt = torch.where(bt < 0, bt, bt + shift).int()
+    mvp.attn_key_weights_paged(c.x[0], kc, torch.tensor(c.lse, device=c.dev), out, c.t32(c.cu_q), sl, bt, block, 40,
+                               c.max_k, scale=w.scale)
+    c.check(out)
+    # ... evicted there, in place
+    new, kept = torch.zeros_like(sl), torch.zeros((2, hkv, 100), dtype=torch.int32, device="cuda")
+    ws = torch.empty(mvp.kv_evict_workspace_size(2, hkv, 100), dtype=torch.uint8, device="cuda")
+    weights = out.cpu().numpy()
+    mvp.kv_evict_paged(kc, kc, out, sl, bt, block, 100, new, kept, ws, c.max_k)
+    torch.cuda.synchronize()
+    for b in range(2):
+        keep = oc.evict(weights[b, 5], w.k_lens[b], 100, 0, 0)
+        assert kept[b, 5].tolist() == keep.tolist()
+        row = lambda j: (int(bt[b, j // block]) - shift) * block + j % block  # noqa: E731
+        src = torch.tensor([row(int(j)) for j in keep], device="cuda")
+        dst = torch.tensor([row(j) for j in range(100)], device="cuda") + shift * block
+        assert torch.equal(kc[dst, 5], small[src, 5])
+
+
 def test_refused_in_python():
     c = Case(_w([4], [9], 2, 2, 64))
     for kw in (dict(weights=torch.zeros((1, 2, 8), device="cuda")),):  # rows shorter than max_k_len

@@ -184,3 +184,20 @@ def test_several_tokens_per_cta(rows, hq, hkv, d, rot):
     c = _case([rows - 400, 1, 0, 399], [rows, 9, 3, 450], hq, hkv, d, rot, 2, 16, torch.bfloat16, rows % 2 == 1,
               seed=rows + rot, pad=3)
     _check(c, *_run(c))
+
+
+def test_far_rows_of_a_large_cache():
+    """Cache rows past 2^32 bytes."""
+    c = _case([70, 1], [300, 20], 2, 8, 128, 64, 2, 256, torch.bfloat16, False, seed=21)
+    ref = _run(c)
+    blocks = 5 * (1 << 30) // (8 * 128 * 2 * 256)
+    shift = blocks - c["k0"].shape[0] // 256
+    big = torch.zeros((blocks * 256, 8, 128), dtype=torch.bfloat16, device="cuda")
+    big[shift * 256:] = c["k0"]
+    vc, q_out = big.clone(), torch.zeros_like(ref[0])
+    vc[shift * 256:] = c["v0"]
+    pos, table, cu, sl, bt, block = c["args"]
+    mvp.rope_append_paged(c["q"], c["k"], c["v"], q_out, big, vc, pos, table, cu, sl, (bt + shift).int(), block)
+    torch.cuda.synchronize()
+    assert torch.equal(q_out, ref[0]) and torch.equal(big[shift * 256:], ref[1]) and torch.equal(vc[shift * 256:], ref[2])
+    assert not big[:shift * 256].any()
