@@ -67,7 +67,8 @@ struct KwParams {
   int skip_decode;         // prefill kernel: leave single-token requests
   int npos;                // query positions per tile
   int n_kb;                // key blocks (prefill) or key chunks (decode) of max_k_len
-  int blocks;              // key blocks one CTA pair takes, one after the other
+  int blocks;              // key blocks one CTA pair takes, one after the other, of
+  int grouped_rows;        // the first (request, KV head, split) rows; one of the others
   int splits;              // parts the query tiles of a key block are shared by
   int max_k_len;
   int* err;
@@ -238,15 +239,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   griddep_wait();
   int x = blockIdx.x >> 1;
   const int n_groups = (p.n_kb + p.blocks - 1) / p.blocks;
-  const int kb0 = (x % n_groups) * p.blocks;
-  x /= n_groups;
+  const bool grouped = x < p.grouped_rows * n_groups;
+  const int per_row = grouped ? n_groups : p.n_kb, blocks = grouped ? p.blocks : 1;
+  if (!grouped) x -= p.grouped_rows * n_groups;
+  const int kb0 = (x % per_row) * blocks;
+  x = x / per_row + (grouped ? 0 : p.grouped_rows);
   const int split = x % p.splits;
   x /= p.splits;
   const int h = x % p.hkv;
   const int b = x / p.hkv + p.req_offset;
   const Req r = load_req<PAGED>(p, b);
   if (kb0 * kTile >= r.k_len || (p.skip_decode && r.q_len == 1)) return;  // (both CTAs)
-  const int kb1 = min(kb0 + p.blocks, (r.k_len + kTile - 1) / kTile);
+  const int kb1 = min(kb0 + blocks, (r.k_len + kTile - 1) / kTile);
   const bool use_table = table_active(p.m);
   const uint32_t* bits = use_table ? sb.range_bits : nullptr;
   const int ncol = p.npos * p.group;  // columns of a CTA's half of a tile that have rows
@@ -973,14 +977,18 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
     while (pp.splits > 1 && one * pp.splits > workspace_bytes) pp.splits /= 2;
     pp.partial = pp.splits > 1 ? static_cast<float*>(workspace) : nullptr;
     // Key blocks per CTA pair: as many as leave four rounds of pairs (the next
-    // block's K loads behind this one's tiles; the pair's set-up is paid once),
-    // at most four: measured on four 2048-row chunks over 0 .. 16384 keys, whose
-    // lengths differ, 305 / 290 / 287 / 286 / 303 us with 1 / 2 / 3 / 4 / 8.
-    // With a range table one, whose tiles are listed at the start.
-    const long long blocks = static_cast<long long>(pp.n_kb) * pp.splits * p.hkv * (num_reqs - first);
+    // block's K loads behind this one's tiles; the pair's set-up, 2 us, is paid
+    // once), at most eight, and single blocks for the last quarter of the rows,
+    // so that the pairs end together (four 2048-row chunks over 0 .. 16384 keys:
+    // 256 us; four blocks everywhere 272, eight 303, one 296).  With a range
+    // table one block, whose tiles are listed at the start.
+    const int rows = pp.splits * p.hkv * (num_reqs - first);
+    const long long blocks = static_cast<long long>(pp.n_kb) * rows;
     pp.blocks = 1;
-    if (range_table == nullptr) pp.blocks = static_cast<int>(std::max(1LL, std::min(4LL, blocks / (2LL * num_sms))));
-    const long long pairs = static_cast<long long>((pp.n_kb + pp.blocks - 1) / pp.blocks) * pp.splits * p.hkv * (num_reqs - first);
+    if (range_table == nullptr) pp.blocks = static_cast<int>(std::max(1LL, std::min(8LL, blocks / (2LL * num_sms))));
+    pp.grouped_rows = rows - rows / 4;
+    const long long pairs = static_cast<long long>((pp.n_kb + pp.blocks - 1) / pp.blocks) * pp.grouped_rows +
+                            static_cast<long long>(pp.n_kb) * (rows - pp.grouped_rows);
     if (2 * pairs > INT_MAX) return MVP_ERR_UNSUPPORTED;
     cudaError_t e = cudaErrorInvalidValue;
     switch (head_dim) {
