@@ -16,7 +16,7 @@
 // streams the query tiles that see any of it, N = 256 columns = 2 x floor(128 /
 // G) positions x G heads, each CTA loading half of them, through a ring of
 // 64-dim chunks (the B operand).  S^T is double-buffered in TMEM; two
-// warpgroups of epilogue warps per CTA each take half of a tile's columns.
+// warpgroups of epilogue warps per CTA share the tiles.
 // * -lse / scale is added by the tensor core: 16 more dims, three of them the
 //   bf16 terms of it (hi + mid + lo, 24 bits) in the columns' operand against
 //   ones in the keys'.  Read from shared memory instead it cost a wavefront per
@@ -119,10 +119,7 @@ __device__ __forceinline__ int2 range_of(const MaskParams& m, const Req& r, int 
 }
 
 // ------------------------------------------------------------------ prefill rows
-// Epilogue warpgroups: each takes half of a tile's columns (four with a quarter
-// each measured 2-8 % slower: the work per tile that every warp repeats).
-constexpr int kEpi = 2;
-constexpr int kEpiCols = 2 * kCols / kEpi;
+constexpr int kEpi = 2;  // epilogue warpgroups
 constexpr int kPfThreads = 128 + 128 * kEpi;  // producer, MMA, column and idle warps, epilogue warps
 constexpr int kMaxTileBits = 4096;
 constexpr int kTile = 2 * kCols;           // columns of a pair's tile
@@ -136,6 +133,15 @@ template <int NCH>
 struct PfCfg {
   static constexpr int KBUF = NCH <= 4 ? 2 : 1;                  // K blocks in shared memory
   static constexpr int STAGES = NCH <= 2 ? 8 : 5;                // Q chunks in flight
+  // The two epilogue warpgroups take the tiles in turn, a buffer each (TURNS),
+  // or half of every tile's columns.  In turn a warp does a tile's bookkeeping
+  // once per 256 columns instead of 128; by halves a buffer is free sooner,
+  // which is what D = 256 needs, where a tile's MMAs take as long as its
+  // exponentials.  Four requests of 16384 + 2048 keys, 16/8 heads, in turn and
+  // by halves: D = 64 491 / 534 us, 128 521 / 543, 256 757 / 651, 512 (chunks over
+  // 0 .. 16384 keys) 443 / 477.
+  static constexpr bool TURNS = NCH != 4;
+  static constexpr int HALVES = TURNS ? 2 : 1;  // halves of a tile a warpgroup takes
   static constexpr int K_BYTES = NCH * kChunkBytes;
   static constexpr int Q_OFF = KBUF * K_BYTES;
   static constexpr int EXT_OFF = Q_OFF + STAGES * kChunkBytes;   // ones, the slots, zeros
@@ -274,9 +280,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&sb.k_full[i], 1);
       mbar_init(&sb.k_empty[i], 1);
       mbar_init(&sb.s_full[i], 1);
-      mbar_init(&sb.s_empty[i], 8 * kEpi);  // both CTAs' epilogue warps (rank 0's barrier)
+      mbar_init(&sb.s_empty[i], C::TURNS ? 8 : 16);  // both CTAs' epilogue warps of the buffer (rank 0's barrier)
       mbar_init(&sb.rng_full[i], 1);
-      mbar_init(&sb.rng_empty[i], 4 * kEpi);
+      mbar_init(&sb.rng_empty[i], C::TURNS ? 4 : 8);  // this CTA's
     }
     for (int i = 0; i < kExt; ++i) {
       mbar_init(&sb.ext_full[i], 2);  // both CTAs' column warps
@@ -490,10 +496,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (!ok) sb.wc.abort = 1;
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- exponentials and sums
-    const int quarter = warp & 3, part = (warp - 4) >> 2;
-    const int half = part / (kEpi / 2), col0 = (part % (kEpi / 2)) * kEpiCols;  // of a half's columns: [col0, col0 + kEpiCols)
+    const int quarter = warp & 3, part = (warp - 4) >> 2;  // the warpgroup
     const int row = quarter * 32 + lane;
-    const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + part * kEpiCols;
+    const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sc = p.m.scale_log2;
     const uint64_t sc2 = f2_pack(sc, sc);
     const uint32_t s_empty0 = mapa_shared(smem_u32(&sb.s_empty[0]), 0);
@@ -516,82 +521,93 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       seen_by(p.m, ja, tmp, in_hi);
       if (jb >= p.m.first_tokens && ja < p.m.first_tokens)
         in_hi = min(in_hi, static_cast<long long>(p.m.first_tokens) + p.m.window_left);
-      // ... that is, the tiles [w_lo, w_hi] whose npos rows of this half all do
+      // ... that is, the tiles [w_lo, w_hi] all of whose npos rows of a half do
       // (64-bit divisions, once per block: done per tile they and the walk took
       // 700 of 2200 clocks a tile).
       const int rows2 = 2 * p.npos;
-      const long long at0 = static_cast<long long>(r.ctx) + half * p.npos;  // position of tile 0's first row of the half
-      const int w_lo = static_cast<int>(max(0LL, min(-floor_div(at0 - in_lo, rows2), 1LL << 30)));
-      int w_hi = static_cast<int>(max(-1LL, min(floor_div(in_hi - at0 - p.npos + 1, rows2),
-                                                floor_div(r.q_len - p.npos - half * p.npos, rows2))));
-      if (key0) w_hi = -1;
+      int w_lo[C::HALVES], w_hi[C::HALVES];
+#pragma unroll
+      for (int e = 0; e < C::HALVES; ++e) {
+        const int half = C::TURNS ? e : part;
+        const long long at0 = static_cast<long long>(r.ctx) + half * p.npos;  // position of tile 0's first row of the half
+        w_lo[e] = static_cast<int>(max(0LL, min(-floor_div(at0 - in_lo, rows2), 1LL << 30)));
+        w_hi[e] = static_cast<int>(max(-1LL, min(floor_div(in_hi - at0 - p.npos + 1, rows2),
+                                                    floor_div(r.q_len - p.npos - half * p.npos, rows2))));
+        if (key0) w_hi[e] = -1;
+      }
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       for (; walk.next(); ++i) {
-        ok = mbar_wait(&sb.s_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
-        if (ok && use_table) ok = mbar_wait(&sb.rng_full[i & 1], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
+        const int buf = i & 1;
+        if (C::TURNS && buf != part) continue;
+        ok = mbar_wait(&sb.s_full[buf], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
+        if (ok && use_table) ok = mbar_wait(&sb.rng_full[buf], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t col = base + (i & 1) * kTile;
         auto release = [&]() {  // the scores are in registers: the buffer is free
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(s_empty0 + (i & 1) * 8);
+          if (lane == 0) mbar_arrive_cluster(s_empty0 + buf * 8);
         };
         const bool ranged = walk.ranged(walk.t);
-        if (walk.t >= w_lo && walk.t <= w_hi && !ranged) {
-          uint32_t s[2][32];
-          tmem_ld_32x32b_x32(col, s[0]);
 #pragma unroll
-          for (int cc = 0; cc < kEpiCols / 32; ++cc) {
-            tmem_ld_wait(s[cc & 1]);
-            if (cc < kEpiCols / 32 - 1) tmem_ld_32x32b_x32(col + 32 * (cc + 1), s[(cc + 1) & 1]);
-            else release();
+        for (int e = 0; e < C::HALVES; ++e) {
+          const int half = C::TURNS ? e : part;
+          const uint32_t col = base + buf * kTile + half * kCols;
+          if (walk.t >= w_lo[e] && walk.t <= w_hi[e] && !ranged) {
+            uint32_t s[2][32];
+            tmem_ld_32x32b_x32(col, s[0]);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              float a0, a1;
-              f2_unpack(f2_mul(f2_pack(__uint_as_float(s[cc & 1][2 * q]), __uint_as_float(s[cc & 1][2 * q + 1])), sc2), a0, a1);
-              acc[q & 3] = f2_add(acc[q & 3], f2_pack(ex2_approx(a0), ex2_approx(a1)));
-            }
-          }
-        } else {
-          const int row0 = (2 * walk.t + half) * p.npos;          // this half's first row
-          const int valid = max(0, min(p.npos, r.q_len - row0));  // rows of the request in it
-          const long long p0 = static_cast<long long>(r.ctx) + row0;
-          // columns of the half that see this thread's key: [c_lo, c_hi]
-          const int c_lo = static_cast<int>(min(max(p_lo - p0, 0LL), static_cast<long long>(valid))) * p.group;
-          const int c_hi = static_cast<int>(min(max(p_hi - p0 + 1, 0LL), static_cast<long long>(valid))) * p.group - 1;
-#pragma unroll 1
-          for (int cc = 0; cc < kEpiCols / 32; ++cc) {
-            uint32_t s[32];
-            tmem_ld_32x32b_x32(col + 32 * cc, s);
-            uint32_t seen = interval_bits(c_lo, c_hi, col0 + 32 * cc);
-            if (ranged && key <= jb) {
-#pragma unroll 8
-              for (int q = 0; q < 32; ++q) {
-                const int2 e = sR[(i & 1) * kTile + part * kEpiCols + 32 * cc + q];
-                seen |= static_cast<uint32_t>(key >= e.x && key <= e.y) << q;
+            for (int cc = 0; cc < kCols / 32; ++cc) {
+              tmem_ld_wait(s[cc & 1]);
+              if (cc < kCols / 32 - 1) tmem_ld_32x32b_x32(col + 32 * (cc + 1), s[(cc + 1) & 1]);
+              else if (e == C::HALVES - 1) release();
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+                float a0, a1;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[cc & 1][2 * q]), __uint_as_float(s[cc & 1][2 * q + 1])), sc2), a0, a1);
+                acc[q & 3] = f2_add(acc[q & 3], f2_pack(ex2_approx(a0), ex2_approx(a1)));
               }
             }
-            tmem_ld_wait(s);
-            if (cc == kEpiCols / 32 - 1) release();
-            if (key0 && key == 0) {
+          } else {
+            const int row0 = (2 * walk.t + half) * p.npos;          // this half's first row
+            const int valid = max(0, min(p.npos, r.q_len - row0));  // rows of the request in it
+            const long long p0 = static_cast<long long>(r.ctx) + row0;
+            // columns of the half that see this thread's key: [c_lo, c_hi]
+            const int c_lo = static_cast<int>(min(max(p_lo - p0, 0LL), static_cast<long long>(valid))) * p.group;
+            const int c_hi = static_cast<int>(min(max(p_hi - p0 + 1, 0LL), static_cast<long long>(valid))) * p.group - 1;
+#pragma unroll 1
+            for (int cc = 0; cc < kCols / 32; ++cc) {
+              uint32_t s[32];
+              tmem_ld_32x32b_x32(col + 32 * cc, s);
+              uint32_t seen = interval_bits(c_lo, c_hi, 32 * cc);
+              if (ranged && key <= jb) {
+#pragma unroll 8
+                for (int q = 0; q < 32; ++q) {
+                  const int2 g = sR[buf * kTile + half * kCols + 32 * cc + q];
+                  seen |= static_cast<uint32_t>(key >= g.x && key <= g.y) << q;
+                }
+              }
+              tmem_ld_wait(s);
+              if (e == C::HALVES - 1 && cc == kCols / 32 - 1) release();
+              if (key0 && key == 0) {
 #pragma unroll
-              for (int q = 0; q < 32; ++q)
-                s[q] = __float_as_uint(__uint_as_float(s[q]) + sb.sink[col0 + 32 * cc + q] / sc);
-            }
+                for (int q = 0; q < 32; ++q)
+                  s[q] = __float_as_uint(__uint_as_float(s[q]) + sb.sink[32 * cc + q] / sc);
+              }
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const float e0 = ex2_approx(__uint_as_float(s[2 * q]) * sc), e1 = ex2_approx(__uint_as_float(s[2 * q + 1]) * sc);
-              acc[q & 3] = f2_add(acc[q & 3], f2_pack((seen >> (2 * q)) & 1u ? e0 : 0.f, (seen >> (2 * q + 1)) & 1u ? e1 : 0.f));
+              for (int q = 0; q < 16; ++q) {
+                const float e0 = ex2_approx(__uint_as_float(s[2 * q]) * sc), e1 = ex2_approx(__uint_as_float(s[2 * q + 1]) * sc);
+                acc[q & 3] = f2_add(acc[q & 3], f2_pack((seen >> (2 * q)) & 1u ? e0 : 0.f, (seen >> (2 * q + 1)) & 1u ? e1 : 0.f));
+              }
             }
           }
         }
         if (use_table) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sb.rng_empty[i & 1]);
+          if (lane == 0) mbar_arrive(&sb.rng_empty[buf]);
         }
       }
-      // a block's sums: the warpgroups' parts of the columns, in their order
+      // a block's sums: the warpgroups' parts, in their order
       float x0, x1, x2, x3;
       f2_unpack(f2_add(acc[0], acc[1]), x0, x1);
       f2_unpack(f2_add(acc[2], acc[3]), x2, x3);
