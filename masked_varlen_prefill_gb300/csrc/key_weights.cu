@@ -17,9 +17,9 @@
 // G) positions x G heads, each CTA loading half of them, through a ring of
 // 64-dim chunks (the B operand).  S^T is double-buffered in TMEM; two
 // warpgroups of epilogue warps per CTA share the tiles.
-// * -lse / scale is added by the tensor core: 16 more dims, three of them the
-//   bf16 terms of it (hi + mid + lo, 24 bits) in the columns' operand against
-//   ones in the keys'.  Read from shared memory instead it cost a wavefront per
+// * -lse / scale is added by the tensor core, relative to one lse per tile (the
+//   exponent's FFMA adds that): 16 more dims, three of them the bf16 terms of it
+//   (hi + mid + lo, 24 bits) in the columns' operand against ones in the keys'.  Read from shared memory instead it cost a wavefront per
 //   column and warp (with operands and copies the shared-memory pipe was full).
 // * Work: 2 D flops and one exponential per visible (row, key) and head; the
 //   exponentials (32 per clock and SM) take half the MMA's time at D = 256 and
@@ -227,6 +227,16 @@ __device__ __forceinline__ uint64_t ext_desc(uint32_t saddr, int zeros) {
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
+// What a tile's columns have their lse relative to: that of its first row and
+// head.  lse / scale is 144 at lse 9 and D = 256, where an fp32 sum keeps 2^-17;
+// its differences within a tile are a few units, like the scores.
+__device__ __forceinline__ float tile_base(const KwParams& p, const Req& r, int h, int t) {
+  const int row = r.q0 + 2 * t * p.npos;
+  if (!in_bounds(row, p.m.total_q, p.err)) return 0.f;
+  const float x = __ldg(p.lse + static_cast<size_t>(h * p.group) * p.m.total_q + row);
+  return fabsf(x) <= kHuge ? x : 0.f;  // (not for an infinity or NaN)
+}
+
 template <int NCH, bool PAGED>
 __global__ void __launch_bounds__(kPfThreads, 1)
     key_weights_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -392,16 +402,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!any) ok = mbar_wait(&sb.k_full[ks], (nb / C::KBUF) & 1, &sb.wc, p.err, kDevTimeoutLoad);
         any = true;
         const int es = i % kExt;
-        if (ok) ok = mbar_wait_spin(&sb.ext_full[es], (i / kExt) & 1, &sb.wc, p.err, kDevTimeoutOther);
         if (ok && i >= 2) ok = mbar_wait_spin(&sb.s_empty[i & 1], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutSoftmax);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (i & 1) * kTile;
         const uint64_t dk = desc_add(dk0, static_cast<uint32_t>((ks * C::K_BYTES) >> 4));
-        if (issuer)
-          mma_ss_one<2>(d, ones, ext_desc(smem_u32(sE + (1 + es) * kExtBytes), (kExt - es) * kExtBytes), idesc, 0u);
-        __syncwarp();
-        mma_commit_elect<2>(&sb.ext_empty[es]);
         for (int c = 0; c < NCH; ++c, ++n) {
           const int s = n % C::STAGES;
           if (!mbar_wait_spin(&sb.q_full[s], (n / C::STAGES) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
@@ -412,12 +417,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
             for (int k16 = 0; k16 < 4; ++k16)
               mma_ss_one<2>(d, desc_add(dk, static_cast<uint32_t>((c * kChunkBytes + k16 * 32) >> 4)),
-                            desc_add(dq, static_cast<uint32_t>((s * kChunkBytes + k16 * 32) >> 4)), idesc, 1u);
+                            desc_add(dq, static_cast<uint32_t>((s * kChunkBytes + k16 * 32) >> 4)), idesc,
+                            (c | k16) != 0 ? 1u : 0u);
           }
           __syncwarp();
           mma_commit_elect<2>(&sb.q_empty[s]);
         }
-        if (ok) mma_commit_elect<2>(&sb.s_full[i & 1]);
+        // the columns' lse last: the products add up among themselves first
+        if (ok) ok = mbar_wait_spin(&sb.ext_full[es], (i / kExt) & 1, &sb.wc, p.err, kDevTimeoutOther);
+        if (!ok) break;
+        if (issuer)
+          mma_ss_one<2>(d, ones, ext_desc(smem_u32(sE + (1 + es) * kExtBytes), (kExt - es) * kExtBytes), idesc, 1u);
+        __syncwarp();
+        mma_commit_elect<2>(&sb.ext_empty[es]);
+        mma_commit_elect<2>(&sb.s_full[i & 1]);
       }
       if (any) {
         if (ok) mma_commit_elect<2>(&sb.k_empty[nb % C::KBUF]);
@@ -431,8 +444,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   } else if (warp == 2) {
     // ---------------------------------------------------------------- columns
     // This lane's columns lane + 32 k of the CTA's half: row within the tile,
-    // and the lse of it.  -lse / scale goes into the column's extension as
-    // three bf16 terms.
+    // and the lse of it.  (base - lse) / scale goes into the column's extension
+    // as three bf16 terms.
     bool ok = true;
     int pos[4];
     const float* src[4];
@@ -442,7 +455,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       pos[k] = c < ncol ? rank * p.npos + c / p.group : INT_MAX / 2;
       src[k] = p.lse + static_cast<size_t>(h * p.group + c % p.group) * p.m.total_q + r.q0 + rank * p.npos + c / p.group;
     }
-    auto load = [&](int t, float (&l)[4]) {
+    auto load = [&](int t, float (&l)[4], float& base) {
+      base = tile_base(p, r, h, t);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int row = 2 * t * p.npos + pos[k];
@@ -454,27 +468,28 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     int i = 0;
     for (int kb = kb0; ok && kb < kb1; ++kb) {
       TileWalk walk = walk_of(p, r, kb, split, bits, false);
-      float l[4], next_l[4];
+      float l[4], next_l[4], base = 0.f, next_base = 0.f;
       bool have = walk.next();
-      if (have) load(walk.t, l);
+      if (have) load(walk.t, l, base);
       for (; ok && have; ++i) {
         const int slot = i & 1, es = i % kExt, t = walk.t;
         // the next tile's loads are in flight while this one waits for its slot
         have = walk.next();
-        if (have) load(walk.t, next_l);
+        if (have) load(walk.t, next_l, next_base);
         if (i >= kExt) ok = mbar_wait(&sb.ext_empty[es], ((i / kExt) - 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
         if (ok && use_table && i >= 2) ok = mbar_wait(&sb.rng_empty[slot], ((i >> 1) - 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
         if (!__all_sync(kFull, ok)) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           // an infinite lse: a weight of zero (or, of -inf, infinity) whatever the score
-          const float v = fabsf(l[k]) == INFINITY ? copysignf(kHuge, -l[k]) : l[k] * inv;
+          const float v = fabsf(l[k]) == INFINITY ? copysignf(kHuge, -l[k]) : (l[k] - base) * inv;
           const float hi = __bfloat162float(__float2bfloat16_rn(v));
           const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
           const uint32_t w0 = pack_bf16x2(hi, mid), w1 = pack_bf16x2((v - hi) - mid, 0.f);
           *reinterpret_cast<uint4*>(sE + (1 + es) * kExtBytes + 16 * (lane + 32 * k)) = make_uint4(w0, w1, 0u, 0u);
           l[k] = next_l[k];
         }
+        base = next_base;
         fence_proxy_async_smem();
         __syncwarp();
         // (released at CTA scope: what the arrival publishes are this CTA's own
@@ -536,9 +551,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (key0) w_hi[e] = -1;
       }
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+      int base_t = -1;  // the tile whose base is loaded, one of this warpgroup's ahead
+      float base_next = 0.f;
       for (; walk.next(); ++i) {
         const int buf = i & 1;
         if (C::TURNS && buf != part) continue;
+        const float shift = -kLog2e * (base_t == walk.t ? base_next : tile_base(p, r, h, walk.t));
+        base_t = walk.t + C::HALVES;
+        if (base_t < walk.t_hi) base_next = tile_base(p, r, h, base_t);
+        const uint64_t shift2 = f2_pack(shift, shift);
         ok = mbar_wait(&sb.s_full[buf], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
         if (ok && use_table) ok = mbar_wait(&sb.rng_full[buf], (i >> 1) & 1, &sb.wc, p.err, kDevTimeoutOther);
         if (!ok) break;
@@ -564,7 +585,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
                 float a0, a1;
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[cc & 1][2 * q]), __uint_as_float(s[cc & 1][2 * q + 1])), sc2), a0, a1);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[cc & 1][2 * q]), __uint_as_float(s[cc & 1][2 * q + 1])), sc2, shift2), a0, a1);
                 acc[q & 3] = f2_add(acc[q & 3], f2_pack(ex2_approx(a0), ex2_approx(a1)));
               }
             }
@@ -596,7 +617,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               }
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
-                const float e0 = ex2_approx(__uint_as_float(s[2 * q]) * sc), e1 = ex2_approx(__uint_as_float(s[2 * q + 1]) * sc);
+                const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * q]), sc, shift));
+                const float e1 = ex2_approx(fmaf(__uint_as_float(s[2 * q + 1]), sc, shift));
                 acc[q & 3] = f2_add(acc[q & 3], f2_pack((seen >> (2 * q)) & 1u ? e0 : 0.f, (seen >> (2 * q + 1)) & 1u ? e1 : 0.f));
               }
             }
