@@ -579,13 +579,14 @@ int mvp_kv_evict_paged(void* k_cache, void* v_cache, const float* weights, float
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cl > 1 ? 1 : 0;
   cfg.gridDim = dim3(static_cast<unsigned>(bh * cl));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = kSelKeys * 4;
   cfg.stream = static_cast<cudaStream_t>(stream);
   if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return MVP_ERR_CUDA;
   cfg.attrs = attr + 1;
+  cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(bh * p.n_segs));
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = 0;

@@ -116,7 +116,8 @@ def test_budgets(budget, first, recent):
     c.check(c.run())
 
 
-@pytest.mark.parametrize("n,reqs", [(4095, 1), (8193, 1), (33000, 1), (70001, 1), (20000, 3)])
+@pytest.mark.parametrize("n,reqs", [(4095, 1), (8193, 1), (33000, 1), (70001, 1), (20000, 3),
+                                    (150001, 1)])
 @pytest.mark.parametrize("kind", ["heavy", "ties"])
 def test_long_requests_shared_by_clusters(n, reqs, kind):
     c = Case([n - 5 * i for i in range(reqs)], 2, 64, 256, n // 3, 4, 128, kind, seed=n)
