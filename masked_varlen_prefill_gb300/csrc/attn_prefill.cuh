@@ -217,9 +217,10 @@ struct Item {
 };
 
 // The item's key tiles: n_first tiles [0, n_first) of first tokens (FIRST
-// kernels; all before kb_lo), then tiles from kb_lo on, n_tiles in all.
+// kernels; all before kb_lo), then tiles from kb_lo on, n_tiles in all.  The
+// last tile of first tokens holds first_k16 times 16 keys that any row sees.
 struct Plan {
-  int kb_lo, n_tiles, int_lo, int_hi, n_first;
+  int kb_lo, n_tiles, int_lo, int_hi, n_first, first_k16;
 };
 
 // Key tile of the item's step j.
@@ -424,7 +425,7 @@ __device__ __forceinline__ Plan plan_tiles(const Item& it, const PrefillParams& 
   hh_max = __reduce_max_sync(kFullMask, hh_max);
   cl_max = __reduce_max_sync(kFullMask, cl_max);
   ch_min = __reduce_min_sync(kFullMask, ch_min);
-  Plan pl{0, 0, 1, 0, 0};
+  Plan pl{0, 0, 1, 0, 0, 0};
   if (hl_min <= hh_max) {
     pl.kb_lo = hl_min / C::BN;
     pl.n_tiles = hh_max / C::BN - pl.kb_lo + 1;
@@ -439,6 +440,7 @@ __device__ __forceinline__ Plan plan_tiles(const Item& it, const PrefillParams& 
     if (pl.n_tiles == 0) pl.kb_lo = nf;
     pl.n_first = min(nf, pl.kb_lo);
     pl.n_tiles += pl.n_first;
+    pl.first_k16 = min(C::BN / 16, (fh_max + 1 - (pl.n_first - 1) * C::BN + 15) / 16);
   }
   return pl;
 }
@@ -863,9 +865,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // Step j issues S_j = Q K_j^T, then O += P V of tile j - LEAD.
         constexpr int LEAD = C::NS - 1;
         for (int j = 0; ok && j < pl.n_tiles + LEAD; ++j) {
+          // The last tile of first tokens usually holds a few keys: its products
+          // cover only those (a pair's MMA takes half its columns from each CTA,
+          // whose tile halves are KROWS keys apart, so the rows' columns past
+          // first_k16 x 16 are of other keys or of an earlier tile: they are
+          // masked like the tile's other keys, and their P, 0, is left out).
+          auto narrow = [&](int jj) { return FIRST && jj == pl.n_first - 1 && pl.first_k16 * 16 <= C::KROWS; };
           if (j < pl.n_tiles) {
             const int t = T + j;
             const int s = t % C::KST;
+            const uint32_t idesc_s =
+                narrow(j) ? idesc_bf16_f32(C::ITEM_ROWS, C::MMA_CTAS * 16 * pl.first_k16, false, false) : idesc_qk;
             if (!mbar_wait_spin(&sb.k_full[s], (t / C::KST) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
               ok = false;
               break;
@@ -879,7 +889,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 for (int k16 = 0; k16 < 4; ++k16) {
                   const uint64_t a = desc_add(dq, static_cast<uint32_t>((c * (kBM * 128) + k16 * 32) >> 4));
                   const uint64_t b = desc_add(dk, static_cast<uint32_t>((c * (C::KROWS * 128) + k16 * 32) >> 4));
-                  mma_ss_one<C::MMA_CTAS>(d, a, b, idesc_qk, (c | k16) != 0 ? 1u : 0u);
+                  mma_ss_one<C::MMA_CTAS>(d, a, b, idesc_s, (c | k16) != 0 ? 1u : 0u);
                 }
               }
             }
@@ -916,9 +926,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const uint32_t pcol = tmem + C::S_COL + C::sbuf(t) * BN;
             const uint64_t dv = desc_add(dv0, static_cast<uint32_t>((s * C::V_STAGE) >> 4));
             const uint32_t first = (j > LEAD) ? 1u : 0u;  // the item's first PV overwrites O
+            const int k16s = narrow(j - LEAD) ? pl.first_k16 : BN / 16;
             if (issuer) {
 #pragma unroll
               for (int kk = 0; kk < BN / 16; ++kk) {
+                if (FIRST && kk >= k16s) break;
                 const uint64_t b = desc_add(dv, static_cast<uint32_t>((kk * 16 * 128) >> 4));
                 mma_ts_one<C::MMA_CTAS>(tmem + C::O_COL, pcol + kk * 8, b, idesc_pv, kk == 0 ? first : 1u);
               }
