@@ -19,8 +19,12 @@
 // warpgroups of epilogue warps per CTA share the tiles.
 // * -lse / scale is added by the tensor core, relative to one lse per tile (the
 //   exponent's FFMA adds that): 16 more dims, three of them the bf16 terms of it
-//   (hi + mid + lo, 24 bits) in the columns' operand against ones in the keys'.  Read from shared memory instead it cost a wavefront per
-//   column and warp (with operands and copies the shared-memory pipe was full).
+//   (hi + mid + lo, 24 bits) in the columns' operand against ones in the keys'.
+//   Read from shared memory instead it cost a wavefront per column and warp
+//   (with operands and copies the shared-memory pipe was full).  A key-0 sink
+//   goes the same way, against ones in the row of key 0 alone: 3 prompts of
+//   1061 tokens, 32/8 heads, D = 256 take 54 us with sinks and 52 without (164
+//   when the epilogue added it, in its masked path).
 // * Work: 2 D flops and one exponential per visible (row, key) and head; the
 //   exponentials (32 per clock and SM) take half the MMA's time at D = 256 and
 //   as long at D = 128.
@@ -124,9 +128,9 @@ constexpr int kPfThreads = 128 + 128 * kEpi;  // producer, MMA, column and idle 
 constexpr int kMaxTileBits = 4096;
 constexpr int kTile = 2 * kCols;           // columns of a pair's tile
 constexpr int kExtBytes = kCols * 16;      // 128 rows x 8 dims of bf16
-// Slots of a tile's -lse / scale: the column warps run up to four tiles ahead of
+// Slots of a tile's -lse / scale: the column warp runs up to three tiles ahead of
 // the MMAs.
-constexpr int kExt = 4;
+constexpr int kExt = 3;
 constexpr float kHuge = 3.0e38f;           // (a bf16 value near it stays finite)
 
 template <int NCH>
@@ -144,15 +148,14 @@ struct PfCfg {
   static constexpr int HALVES = TURNS ? 2 : 1;  // halves of a tile a warpgroup takes
   static constexpr int K_BYTES = NCH * kChunkBytes;
   static constexpr int Q_OFF = KBUF * K_BYTES;
-  static constexpr int EXT_OFF = Q_OFF + STAGES * kChunkBytes;   // ones, the slots, zeros
-  static constexpr int ZERO_OFF = EXT_OFF + (1 + kExt) * kExtBytes;
+  static constexpr int EXT_OFF = Q_OFF + STAGES * kChunkBytes;   // the keys' two parts, the slots, zeros
+  static constexpr int ZERO_OFF = EXT_OFF + (2 + kExt) * kExtBytes;
   static constexpr int RNG_OFF = ZERO_OFF + kExtBytes;           // two slots of kTile intervals
   static constexpr int SHARED_OFF = RNG_OFF + 2 * kTile * 8;
 };
 
 struct __align__(16) PfShared {
   uint32_t range_bits[kMaxTileBits / 32];  // tiles with a row whose range meets this key block
-  float sink[kCols];                       // key-0 sinks of a CTA's columns, log2 units
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full[8], q_empty[8];
   uint64_t ext_full[kExt], ext_empty[kExt];
@@ -312,13 +315,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tmem_relinquish_pair();
   }
   // Operand parts that nothing else writes: ones in the first three dims of the
-  // keys' extension, the zeros of dims 8 .. 15, and zeros in the rows of a Q
-  // chunk past the last column.
+  // keys' extension (and, for the block of key 0, in that key's next three,
+  // which take the columns' sinks), the zeros of dims 8 .. 15, and zeros in the
+  // rows of a Q chunk past the last column.
   for (int i = threadIdx.x; i < kCols; i += kPfThreads) {
+    const bool first_key = rank == 0 && i == 0;
     *reinterpret_cast<uint4*>(sE + 16 * i) = make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u);
+    *reinterpret_cast<uint4*>(sE + kExtBytes + 16 * i) =
+        make_uint4(0x3F803F80u, first_key ? 0x3F803F80u : 0x00003F80u, first_key ? 0x3F803F80u : 0u, 0u);
     *reinterpret_cast<uint4*>(smem + C::ZERO_OFF + 16 * i) = make_uint4(0, 0, 0, 0);
-    const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr && i < ncol;
-    sb.sink[i] = key0 ? __ldg(p.m.sinks + h * p.group + i % p.group) * kLog2e : 0.f;
   }
   if (ncol < kCols) {
     const int words = (kCols - ncol) * 8;  // 16-byte words at the end of each chunk
@@ -390,13 +395,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     constexpr uint32_t idesc = idesc_bf16_f32(2 * kKeys, kTile, false, false);
     const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t ones = ext_desc(smem_u32(sE), C::ZERO_OFF - C::EXT_OFF);
     const bool issuer = elect_one();
     bool ok = true;
     int n = 0, nb = 0, i = 0;  // chunks, K blocks, tiles
     for (int kb = kb0; ok && kb < kb1; ++kb) {
       TileWalk walk = walk_of(p, r, kb, split, bits, false);
       bool any = false;
+      const int part = kb == 0 ? 1 : 0;  // the keys' extension
+      const uint64_t keys = ext_desc(smem_u32(sE + part * kExtBytes), (2 + kExt - part) * kExtBytes);
       for (; ok && walk.next(); ++i) {
         const int ks = nb % C::KBUF;
         if (!any) ok = mbar_wait(&sb.k_full[ks], (nb / C::KBUF) & 1, &sb.wc, p.err, kDevTimeoutLoad);
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (ok) ok = mbar_wait_spin(&sb.ext_full[es], (i / kExt) & 1, &sb.wc, p.err, kDevTimeoutOther);
         if (!ok) break;
         if (issuer)
-          mma_ss_one<2>(d, ones, ext_desc(smem_u32(sE + (1 + es) * kExtBytes), (kExt - es) * kExtBytes), idesc, 1u);
+          mma_ss_one<2>(d, keys, ext_desc(smem_u32(sE + (2 + es) * kExtBytes), (kExt - es) * kExtBytes), idesc, 1u);
         __syncwarp();
         mma_commit_elect<2>(&sb.ext_empty[es]);
         mma_commit_elect<2>(&sb.s_full[i & 1]);
@@ -447,11 +453,25 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // and the lse of it.  (base - lse) / scale goes into the column's extension
     // as three bf16 terms.
     bool ok = true;
+    // The key-0 sinks (key-0-bias mode), in units of the score, go there the same
+    // way, against the ones of key 0 alone.
+    const float inv = -1.f / p.m.scale;
     int pos[4];
     const float* src[4];
+    uint32_t sink1[4], sink2[4];  // terms (0, hi) and (mid, lo)
+    auto bf16 = [](float x) { return __bfloat162float(__float2bfloat16_rn(x)); };
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int c = lane + 32 * k;
+      float x = 0.f;
+      if (p.m.sink_mode == 1 && p.m.sinks != nullptr && c < ncol) {
+        const float s0 = __ldg(p.m.sinks + h * p.group + c % p.group);
+        // (a NaN reaches the rows of key 0 through their lse; here it would
+        // meet the other keys' zeros)
+        x = isnan(s0) ? 0.f : fabsf(s0) == INFINITY ? copysignf(kHuge, s0) : -s0 * inv;
+      }
+      sink1[k] = pack_bf16x2(0.f, x);
+      sink2[k] = pack_bf16x2(x - bf16(x), (x - bf16(x)) - bf16(x - bf16(x)));
       pos[k] = c < ncol ? rank * p.npos + c / p.group : INT_MAX / 2;
       src[k] = p.lse + static_cast<size_t>(h * p.group + c % p.group) * p.m.total_q + r.q0 + rank * p.npos + c / p.group;
     }
@@ -463,7 +483,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         l[k] = row < r.q_len && in_bounds(r.q0 + row, p.m.total_q, p.err) ? __ldg(src[k] + 2 * t * p.npos) : INFINITY;
       }
     };
-    const float inv = -1.f / p.m.scale;
     const uint32_t ext_bar = mapa_shared(smem_u32(&sb.ext_full[0]), 0);
     int i = 0;
     for (int kb = kb0; ok && kb < kb1; ++kb) {
@@ -483,10 +502,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int k = 0; k < 4; ++k) {
           // an infinite lse: a weight of zero (or, of -inf, infinity) whatever the score
           const float v = fabsf(l[k]) == INFINITY ? copysignf(kHuge, -l[k]) : (l[k] - base) * inv;
-          const float hi = __bfloat162float(__float2bfloat16_rn(v));
-          const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
+          const float hi = bf16(v), mid = bf16(v - hi);
           const uint32_t w0 = pack_bf16x2(hi, mid), w1 = pack_bf16x2((v - hi) - mid, 0.f);
-          *reinterpret_cast<uint4*>(sE + (1 + es) * kExtBytes + 16 * (lane + 32 * k)) = make_uint4(w0, w1, 0u, 0u);
+          *reinterpret_cast<uint4*>(sE + (2 + es) * kExtBytes + 16 * (lane + 32 * k)) =
+              make_uint4(w0, w1 | sink1[k], sink2[k], 0u);
           l[k] = next_l[k];
         }
         base = next_base;
@@ -526,7 +545,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     for (int kb = kb0; kb < kb1; ++kb) {
       TileWalk walk = walk_of(p, r, kb, split, bits, false);
       const int ja = walk.ja + rank * kKeys, jb = min(ja + kKeys - 1, walk.jb), key = ja + row;  // this CTA's keys
-      const bool key0 = p.m.sink_mode == 1 && p.m.sinks != nullptr && ja == 0;
       long long p_lo, p_hi;
       seen_by(p.m, key, p_lo, p_hi);
       if (key > jb) p_hi = p_lo - 1;
@@ -548,7 +566,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         w_lo[e] = static_cast<int>(max(0LL, min(-floor_div(at0 - in_lo, rows2), 1LL << 30)));
         w_hi[e] = static_cast<int>(max(-1LL, min(floor_div(in_hi - at0 - p.npos + 1, rows2),
                                                     floor_div(r.q_len - p.npos - half * p.npos, rows2))));
-        if (key0) w_hi[e] = -1;
       }
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       int base_t = -1;  // the tile whose base is loaded, one of this warpgroup's ahead
@@ -610,11 +627,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               }
               tmem_ld_wait(s);
               if (e == C::HALVES - 1 && cc == kCols / 32 - 1) release();
-              if (key0 && key == 0) {
-#pragma unroll
-                for (int q = 0; q < 32; ++q)
-                  s[q] = __float_as_uint(__uint_as_float(s[q]) + sb.sink[32 * cc + q] / sc);
-              }
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
                 const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * q]), sc, shift));

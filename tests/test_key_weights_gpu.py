@@ -133,6 +133,22 @@ def test_single_tokens(d, hq, hkv, window, first):
     assert torch.equal(a, Case(w, first).run(n_dec=6))
 
 
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("q,k", [([130, 300], [400, 301]), ([1, 1], [300, 2])])
+def test_key0_sinks_far_apart(d, q, k, monkeypatch):
+    """A sink that closes key 0, one that takes nearly all of the weight, and
+    small ones, in one tile."""
+    inputs = gh.make_inputs
+
+    def far(w):
+        x = inputs(w)
+        x[3].copy_(torch.tensor([-np.inf, 40.0, -7.5, 0.0]))
+        return x
+
+    monkeypatch.setattr(gh, "make_inputs", far)
+    Case(_w(q, k, 4, 1, d, -1, sink=1, seed=d)).check_all(16)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_masks(seed):
     rng = np.random.RandomState(seed)
