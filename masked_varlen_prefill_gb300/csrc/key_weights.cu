@@ -762,8 +762,29 @@ __global__ void __launch_bounds__(kDecThreads)
       const int run = PAGED ? min(kKeys, 1 << p.m.block_shift) : kKeys;
       mbar_arrive_expect_tx(&sb.q_full, static_cast<uint32_t>(NCH * p.group * 128));
       for (int x = 0; x < NCH; ++x) tma_load_3d(sQ + x * n * 128, &map_q, &sb.q_full, x * 64, h * p.group, r.q0);
-      for (int i = 0; ok && i < tiles; ++i) {
-        if (!meets(i)) continue;
+      // Cache rows of a tile's runs (paged), looked up a tile ahead: the block
+      // ids' latency is then not in the way of a freed stage.
+      constexpr int kRuns = PAGED ? kKeys / 16 : 1;
+      int next[kRuns];
+      auto look_up = [&](int i) {
+        if constexpr (PAGED) {
+#pragma unroll
+          for (int k = 0; k < kRuns; ++k)
+            if (k * run < kKeys) next[k] = kv_row(p.m, b, 0, r.k_len, key_lo + i * kKeys + k * run);
+        }
+      };
+      auto next_tile = [&](int i) {
+        while (i < tiles && !meets(i)) ++i;
+        return i;
+      };
+      int i = next_tile(0);
+      if (i < tiles) look_up(i);
+      while (ok && i < tiles) {
+        int rows[kRuns];
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) rows[k] = next[k];
+        const int after = next_tile(i + 1);
+        if (after < tiles) look_up(after);
         for (int x = 0; x < NCH; ++x, ++c) {
           const int s = c % kDecStages;
           if (c >= kDecStages && !mbar_wait(&sb.k_empty[s], ((c / kDecStages) - 1) & 1, &sb.wc, p.err, kDevTimeoutLoad)) {
@@ -771,12 +792,14 @@ __global__ void __launch_bounds__(kDecThreads)
             break;
           }
           mbar_arrive_expect_tx(&sb.k_full[s], kChunkBytes);
-          for (int k = 0; k < kKeys; k += run) {
-            const int key = key_lo + i * kKeys + k;
-            const int row = PAGED ? kv_row(p.m, b, 0, r.k_len, key) : r.k0 + key;
-            tma_load_3d(sK + s * kChunkBytes + k * 128, &map_k, &sb.k_full[s], x * 64, h, row);
+#pragma unroll
+          for (int k = 0; k < kRuns; ++k) {
+            if (k * run >= kKeys) break;
+            const int row = PAGED ? rows[k] : r.k0 + key_lo + i * kKeys;
+            tma_load_3d(sK + s * kChunkBytes + k * run * 128, &map_k, &sb.k_full[s], x * 64, h, row);
           }
         }
+        i = after;
       }
       if (!ok) sb.wc.abort = 1;
       WaitCtl own = own_wait_ctl(&sb.wc);
