@@ -7,13 +7,18 @@
 //
 // 1. evict_select_kernel finds, per (request, KV head), the weight of rank
 //    budget - first - recent by a radix select over order-preserving integer
-//    keys (11, 11 and 10 bits: three histograms in shared memory), then lists
-//    the kept keys in order with a block-wide prefix sum.  Integer counts
+//    keys (11, 11 and 10 bits: three histograms in shared memory, or fewer
+//    where all of a bin stays), then lists the kept keys in order: a bit per
+//    key from warp votes, and a prefix sum of their counts.  Integer counts
 //    only, so the result does not depend on the order of the atomics.  Long
 //    requests are shared by a cluster of CTAs, which add their histograms
 //    through distributed shared memory.  It reads 4 bytes of each key's
 //    weight (from L2 after the first time), against 4 * D bytes of K and V
-//    that the move reads and writes for a kept one.
+//    that the move reads and writes for a kept one.  Bound by its instructions
+//    (about 40 per 32 keys) and by what a pass costs whatever the keys (1500
+//    cycles; 900 instructions per warp in all): 48 requests of 4096 to 32768
+//    keys, 8 KV heads, 40 us (four compares and a prefix sum per key in place
+//    of the votes, and always three passes: 50).
 // 2. evict_move_kernel copies the kept rows, 32 KB per CTA, all of it in flight
 //    at once in registers (bulk copies of single rows measured slower: at 256
 //    bytes each they queue for the copy engine).  It is bound by memory.  In
@@ -45,6 +50,7 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 16384;  // keys a CTA holds in shared memory (the rest is read again from L2)
 constexpr int kBins = 2048;
+constexpr unsigned kFullWarp = 0xffffffffu;
 constexpr uint32_t kStays = 0xffffffffu;  // order key of a key that stays whatever its weight
 static_assert(kBins == 4 * kSelThreads, "four bins per thread");
 constexpr int kMoveThreads = 256;
@@ -87,8 +93,8 @@ __device__ __forceinline__ long long weight_row(const EvictParams& p, int b, int
 
 // Larger key, heavier weight; -0 and +0 are equal, NaN is -inf.
 __device__ __forceinline__ uint32_t order_key(float w) {
-  const uint32_t u = __float_as_uint(w != w ? -INFINITY : w + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(w, -INFINITY) + 0.0f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -116,10 +122,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   extern __shared__ __align__(16) uint32_t s_key[];  // [kSelKeys] order keys of the CTA's first keys
   __shared__ __align__(16) int s_hist[kBins];
   __shared__ int s_warp[kSelWarps][2];
-  __shared__ int s_bin, s_need;
+  __shared__ int s_bin, s_need, s_in;
   __shared__ int s_count[2];
   const int cl = static_cast<int>(cluster_size()), c = static_cast<int>(cluster_rank());
-  const int bh = blockIdx.x / cl, b = bh / p.hkv, h = bh % p.hkv;
+  const int cl_shift = __popc(cl - 1);  // (a power of two)
+  const int bh = blockIdx.x >> cl_shift, b = bh / p.hkv, h = bh - b * p.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto sync = [&]() {
     if (cl > 1) cluster_sync_all();
@@ -141,21 +148,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const float* w = p.w + wrow;
   const int lo = p.first, hi = n - p.recent;  // the keys that compete
   // This CTA's keys [s0, s1), each warp's a run of `per` of them.
-  const int per = ((n + cl * kSelWarps - 1) / (cl * kSelWarps) + 127) / 128 * 128;
+  static_assert((kSelWarps & (kSelWarps - 1)) == 0, "a power of two");
+  const int round = 128 * kSelWarps * cl;
+  const int per = ((n + round - 1) >> (cl_shift + __popc(128 * kSelWarps - 1))) * 128;
   const int s0 = min(n, c * per * kSelWarps), s1 = min(n, s0 + per * kSelWarps);
   const int size = per * kSelWarps;
-  // Order key of the CTA's i-th key: kStays for those that stay anyway, 0 past
-  // the last one (order keys of weights lie strictly between).
-  auto encode = [&](int i) -> uint32_t {
-    const int k = s0 + i;
-    if (k >= s1) return 0u;
-    return (k < lo || k >= hi) ? kStays : order_key(w[k]);
+  const uint32_t span = static_cast<uint32_t>(hi - lo);
+  // Order key of key k, of weight x: kStays for those that stay anyway, 0 past
+  // the CTA's last one (order keys of weights lie strictly between).
+  auto encode = [&](int k, float x) -> uint32_t {
+    const uint32_t key = static_cast<uint32_t>(k - lo) < span ? order_key(x) : kStays;
+    return k < s1 ? key : 0u;
   };
-  // Four of them, i a multiple of 4.
-  auto keys4 = [&](int i) -> uint4 {
-    if (i < kSelKeys) return *reinterpret_cast<const uint4*>(s_key + i);
-    return make_uint4(encode(i), encode(i + 1), encode(i + 2), encode(i + 3));
-  };
+  auto read = [&](int i) -> uint32_t { return encode(s0 + i, w[min(s0 + i, n - 1)]); };
 
   // ------------------------------------------------ the weight of that rank
   // Every key once from memory, into shared memory and the first histogram.
@@ -163,18 +168,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   __syncthreads();
   // Eight loads in flight per thread.
   constexpr int kAhead = 8;
-  for (int i = tid; i < size; i += kAhead * kSelThreads) {
+  for (int i0 = 0; i0 < size; i0 += kAhead * kSelThreads) {
+    const int k = s0 + i0 + tid;
     float x[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) x[u] = w[min(s0 + i + u * kSelThreads, n - 1)];
+    for (int u = 0; u < kAhead; ++u) x[u] = k + u * kSelThreads < s1 ? w[k + u * kSelThreads] : 0.f;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int at = i + u * kSelThreads, k = s0 + at;
-      if (at < size) {
-        const uint32_t key = k >= s1 ? 0u : ((k < lo || k >= hi) ? kStays : order_key(x[u]));
-        if (at < kSelKeys) s_key[at] = key;
-        atomicAdd(&s_hist[key >> 21], 1);
-      }
+      const int at = i0 + u * kSelThreads;  // (the same for all threads; size and kSelKeys are multiples)
+      if (at >= size) break;
+      const uint32_t key = encode(k + u * kSelThreads, x[u]);
+      if (at < kSelKeys) s_key[at + tid] = key;
+      atomicAdd(&s_hist[key >> 21], 1);
     }
   }
   uint32_t prefix = kStays - 1u, mask = 0u;  // (no weight's key: none competes when none may stay)
@@ -186,15 +191,25 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
       const uint32_t digit = pass == 2 ? 1023u : kBins - 1u;
       if (pass > 0) {
-        *reinterpret_cast<int4*>(&s_hist[4 * tid]) = make_int4(0, 0, 0, 0);
-        __syncthreads();
+        if (cl > 1) {  // (a CTA alone has cleared them as it read them)
+          *reinterpret_cast<int4*>(&s_hist[4 * tid]) = make_int4(0, 0, 0, 0);
+          __syncthreads();
+        }
+        auto add = [&](uint4 k) {
+          const bool in[4] = {(k.x & mask) == prefix, (k.y & mask) == prefix, (k.z & mask) == prefix,
+                              (k.w & mask) == prefix};
+          if (!(in[0] || in[1] || in[2] || in[3])) return;
+          if (in[0]) atomicAdd(&s_hist[(k.x >> shift) & digit], 1);
+          if (in[1]) atomicAdd(&s_hist[(k.y >> shift) & digit], 1);
+          if (in[2]) atomicAdd(&s_hist[(k.z >> shift) & digit], 1);
+          if (in[3]) atomicAdd(&s_hist[(k.w >> shift) & digit], 1);
+        };
 #pragma unroll 2
-        for (int i = 4 * tid; i < size; i += 4 * kSelThreads) {
-          const uint4 k = keys4(i);
-          if ((k.x & mask) == prefix) atomicAdd(&s_hist[(k.x >> shift) & digit], 1);
-          if ((k.y & mask) == prefix) atomicAdd(&s_hist[(k.y >> shift) & digit], 1);
-          if ((k.z & mask) == prefix) atomicAdd(&s_hist[(k.z >> shift) & digit], 1);
-          if ((k.w & mask) == prefix) atomicAdd(&s_hist[(k.w >> shift) & digit], 1);
+        for (int at = 0; at < min(size, kSelKeys); at += 4 * kSelThreads)
+          add(*reinterpret_cast<const uint4*>(s_key + at + 4 * tid));
+        for (int at = kSelKeys; at < size; at += 4 * kSelThreads) {
+          const int i = at + tid;
+          add(make_uint4(read(i), read(i + kSelThreads), read(i + 2 * kSelThreads), read(i + 3 * kSelThreads)));
         }
       }
       sync();
@@ -204,6 +219,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       int4 q;
       if (cl == 1) {
         q = *reinterpret_cast<const int4*>(&s_hist[bin0]);
+        *reinterpret_cast<int4*>(&s_hist[bin0]) = make_int4(0, 0, 0, 0);
       } else {
         q = make_int4(0, 0, 0, 0);
         for (int r = 0; r < cl; ++r) {
@@ -214,26 +230,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       if (pass == 0 && tid == 0) q.w = 0;                // keys that stay anyway
       if (pass == 0 && tid == kSelThreads - 1) q.x = 0;  // past the last key
       const int cnt[4] = {q.w, q.z, q.y, q.x}, sum = q.x + q.y + q.z + q.w;
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31) s_warp[warp][0] = incl;
+      // The warp that the rank falls into finds the bin.
+      const int warp_sum = __reduce_add_sync(kFullWarp, sum);
+      if (lane == 0) s_warp[warp][0] = warp_sum;
       __syncthreads();
-      const int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane & (kSelWarps - 1)][0] : 0);
-      if (before < need && need <= before + sum) {  // one thread
-        int at = before, i = 0;
-        while (at + cnt[i] < need) at += cnt[i++];
-        s_bin = bin0 + 3 - i;
-        s_need = need - at;
+      const int warp_before = __reduce_add_sync(kFullWarp, lane < warp ? s_warp[lane & (kSelWarps - 1)][0] : 0);
+      if (warp_before < need && need <= warp_before + warp_sum) {
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(kFullWarp, incl, o);
+          if (lane >= o) incl += x;
+        }
+        const int before = warp_before + incl - sum;
+        if (before < need && need <= before + sum) {  // one thread
+          int at = before, i = 0;
+          while (at + cnt[i] < need) at += cnt[i++];
+          s_bin = bin0 + 3 - i;
+          s_need = need - at;
+          s_in = cnt[i];
+        }
       }
       __syncwarp();
       sync();  // (also: every CTA has read the others' counts)
       prefix |= static_cast<uint32_t>(s_bin) << shift;
       mask |= digit << shift;
       need = s_need;
+      if (need == s_in) {  // every key of the bin stays: no need to look into it
+        prefix -= 1u;
+        need = 0;
+        break;
+      }
     }
   } else {
     __syncthreads();  // s_key is complete
@@ -241,24 +268,42 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 
   // ------------------------------------------------ the kept keys, in order
   // Keys above the prefix stay, and the first `need` of those equal to it.
+  // 1024 of the warp's keys at a time: lane u takes the votes on the u-th 32 of
+  // them, a bit per key.
+  const int i0 = __shfl_sync(kFullWarp, warp, 0) * per;  // (known to be the warp's own)
+  unsigned above = 0, equal = 0;
+  auto vote = [&](int at) {
+    above = equal = 0;
+    const int words = min(32, (i0 + per - at) / 32);
+    auto take = [&](int u, uint32_t k) {
+      const unsigned g = __ballot_sync(kFullWarp, k > prefix), e = __ballot_sync(kFullWarp, k == prefix);
+      if (lane == u) {
+        above = g;
+        equal = e;
+      }
+    };
+    const int held = min(words, max(0, kSelKeys - at) / 32);  // (the first keys, in shared memory)
+#pragma unroll 4
+    for (int u = 0; u < held; ++u) take(u, s_key[at + 32 * u + lane]);
+#pragma unroll 4
+    for (int u = held; u < words; ++u) take(u, read(at + 32 * u + lane));
+  };
   // Their numbers in this warp's run, then before it.
-  const int i0 = warp * per;
   int g = 0, tie = 0;
-#pragma unroll 2
-  for (int i = i0 + 4 * lane; i < i0 + per; i += 128) {
-    const uint4 k = keys4(i);
-    g += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
-    tie += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
+  for (int at = i0; at < i0 + per; at += 1024) {
+    vote(at);
+    g += __popc(above);
+    tie += __popc(equal);
   }
-  g = __reduce_add_sync(0xffffffffu, g);
-  tie = __reduce_add_sync(0xffffffffu, tie);
+  g = __reduce_add_sync(kFullWarp, g);
+  tie = __reduce_add_sync(kFullWarp, tie);
   if (lane == 0) {
     s_warp[warp][0] = g;
     s_warp[warp][1] = tie;
   }
   __syncthreads();
-  int gb = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane & (kSelWarps - 1)][0] : 0);
-  int tb = __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane & (kSelWarps - 1)][1] : 0);
+  int gb = __reduce_add_sync(kFullWarp, lane < warp ? s_warp[lane & (kSelWarps - 1)][0] : 0);
+  int tb = __reduce_add_sync(kFullWarp, lane < warp ? s_warp[lane & (kSelWarps - 1)][1] : 0);
   if (cl > 1) {
     if (tid == kSelThreads - 1) {
       s_count[0] = gb + g;
@@ -271,40 +316,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
       tb += ld_cluster_s32(mapa_shared(smem_u32(&s_count[1]), r));
     }
   }
-  const unsigned below = (1u << lane) - 1u;
-#pragma unroll 2
-  for (int i = i0 + 4 * lane; i < i0 + per; i += 128) {
-    const uint4 k4 = keys4(i);
-    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-    unsigned bg[4], at_g = gb, ties = 0;
+  for (int at = i0; at < i0 + per; at += 1024) {
+    if (per > 1024) vote(at);  // (else the votes are still here)
+    const int own = __popc(above) | __popc(equal) << 16;
+    int incl = own;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      bg[q] = __ballot_sync(0xffffffffu, k[q] > prefix);
-      at_g += __popc(bg[q] & below);
-      ties |= k[q] == prefix;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFullWarp, incl, o);
+      if (lane >= o) incl += x;
     }
-    // Ties (few, unless many weights are equal) are counted apart; of those
-    // before this lane's keys the first `need` stay.
-    int at_t = tb;
-    if (__any_sync(0xffffffffu, ties)) {
-      int all = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const unsigned be = __ballot_sync(0xffffffffu, k[q] == prefix);
-        at_t += __popc(be & below);
-        all += __popc(be);
-      }
-      tb += all;
+    const int t0 = tb + ((incl - own) >> 16), room = max(need - t0, 0);
+    if (room == 0) equal = 0;
+    while (__popc(equal) > room) equal &= ~(1u << (31 - __clz(equal)));  // the highest goes first
+    // Listed in shared memory, where these keys were (nobody reads them again),
+    // and from there to `kept` in whole lines: 16384 keys cut to 8192, 384 times,
+    // take 72000 cycles with each lane storing its own.  Keys past those held
+    // there are few words of long requests.
+    const int all = __shfl_sync(kFullWarp, incl, 31);
+    const int start = gb + min(tb, need), count = (all & 0xffff) + min(tb + (all >> 16), need) - min(tb, need);
+    const bool held = at + 1024 <= kSelKeys;
+    int to = ((incl - own) & 0xffff) + min(t0, need) - min(tb, need);
+    __syncwarp();
+    for (unsigned stay = above | equal; stay != 0; stay &= stay - 1, ++to) {
+      const int k = s0 + at + 32 * lane + __ffs(stay) - 1;
+      if (held) s_key[at + to] = k;
+      else if (start + to < p.budget) kept[start + to] = k;
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool above = k[q] > prefix, equal = k[q] == prefix;
-      const int at = static_cast<int>(at_g) + min(at_t, need);
-      if ((above || (equal && at_t < need)) && at < p.budget) kept[at] = s0 + i + q;
-      at_g += above;
-      at_t += equal;
-      gb += __popc(bg[q]);
-    }
+    __syncwarp();
+    if (held)
+      for (int i = lane; i < min(count, p.budget - start); i += 32) kept[start + i] = s_key[at + i];
+    gb += all & 0xffff;
+    tb += all >> 16;
   }
   // (Here, not at the start: move CTAs waiting next to the second wave of these
   // cost 45 us of 400 on a batch of 384 (request, KV head) pairs.)
@@ -343,9 +385,9 @@ __device__ __forceinline__ void add_release(int* ptr, int v) {
 // A CTA per segment; its warps take wr rows each and share nothing but the
 // ticket, so that each goes through kept keys -> block ids -> rows -> flag ->
 // stores at its own pace.  A segment's flag counts the warps that have loaded.
-// 48 requests cut to 4096 keys of 8 KV heads at D = 128 (1.6 GB moved): 296 us,
-// 0.83 of the copy rate with the four CTAs an SM holds at 56 registers, 14 us
-// less with five.
+// 48 requests cut to 4096 keys of 8 KV heads at D = 128 (1.6 GB moved): 284 us,
+// 0.86 of the copy rate, with five CTAs per SM (296 with the four that 56
+// registers allow).
 __global__ void __launch_bounds__(kMoveThreads, 5) evict_move_kernel(const EvictParams p) {
   __shared__ int s_ticket;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
