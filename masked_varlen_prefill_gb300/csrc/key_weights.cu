@@ -33,9 +33,14 @@
 //   columns; tiles seen whole skip it.  Only range-table rows need a test per
 //   column, in the tiles that hold such a row.
 //
-// Single-token rows: K is streamed (the A operand, 64-dim chunks of 128 keys),
-// the row's G heads are the B operand (N = G rounded up to 16); bound by the
-// one read of K.
+// Single tokens, and calls whose requests all have few rows (a drafted
+// continuation to verify): K is streamed (the A operand, 64-dim chunks of 128
+// keys), the rows' G heads are the B operand (N = rows x G rounded up to 16, at
+// most 128); bound by the one read of K, and past some 48 columns by a chain of
+// one exponential per column in four warps.  64 requests of 4096 .. 8192 keys,
+// 32/8 heads, D = 128: 131 us with 1 or 4 rows, 239 with 16, 400 with 32
+// (floor 124); 946 in the prefill kernel, whose tiles of 256 columns they leave
+// mostly empty.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -191,7 +196,12 @@ struct TileWalk {
   }
 };
 
-__device__ __forceinline__ long long floor_div(long long a, int b) { return a >= 0 ? a / b : -((-a + b - 1) / b); }
+// (b > 0; a 64-bit division costs four of 32 bits, and most fit)
+__device__ __forceinline__ long long floor_div(long long a, int b) {
+  const unsigned long long u = a >= 0 ? a : -a + b - 1;
+  const long long x = (u >> 32) == 0 ? static_cast<unsigned>(u) / static_cast<unsigned>(b) : u / b;
+  return a >= 0 ? x : -x;
+}
 
 // bits: the block's range bits, or null; whole: before the split.
 __device__ __forceinline__ TileWalk walk_of(const KwParams& p, const Req& r, int kb, int split, const uint32_t* bits,
@@ -519,7 +529,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (use_table) {
           if (walk.ranged(t))
             for (int c = lane; c < kTile; c += 32) {
-              const int half = c / kCols, cc = c % kCols, row = (2 * t + half) * p.npos + cc / p.group;
+              const int half = c / kCols, cc = c % kCols, row0 = (2 * t + half) * p.npos;
+              if ((r.q_len - row0) * static_cast<long long>(p.group) <= cc - lane) continue;  // (32 columns of no row: not read)
+              const int row = row0 + cc / p.group;
               sR[slot * kTile + c] = (cc < ncol && row < r.q_len) ? range_of(p.m, r, row) : make_int2(1, 0);
             }
           __syncwarp();
@@ -613,8 +625,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             // columns of the half that see this thread's key: [c_lo, c_hi]
             const int c_lo = static_cast<int>(min(max(p_lo - p0, 0LL), static_cast<long long>(valid))) * p.group;
             const int c_hi = static_cast<int>(min(max(p_hi - p0 + 1, 0LL), static_cast<long long>(valid))) * p.group - 1;
+            const int n_cc = (valid * p.group + 31) / 32;  // (32 columns at a time, of rows)
+            if (e == C::HALVES - 1 && n_cc == 0) release();
 #pragma unroll 1
-            for (int cc = 0; cc < kCols / 32; ++cc) {
+            for (int cc = 0; cc < n_cc; ++cc) {
               uint32_t s[32];
               tmem_ld_32x32b_x32(col + 32 * cc, s);
               uint32_t seen = interval_bits(c_lo, c_hi, 32 * cc);
@@ -626,7 +640,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
               }
               tmem_ld_wait(s);
-              if (e == C::HALVES - 1 && cc == kCols / 32 - 1) release();
+              if (e == C::HALVES - 1 && cc == n_cc - 1) release();
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
                 const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * q]), sc, shift));
@@ -683,7 +697,8 @@ __global__ void __launch_bounds__(256) key_weights_combine_kernel(const KwParams
   if (w != nullptr) w[key] = p.accumulate ? w[key] + total : total;
 }
 
-// ------------------------------------------------------------------ single-token rows
+// ------------------------------------------------------------------ requests of few rows
+constexpr int kFewCols = 128;  // columns (rows x heads) of a request this kernel takes, at most
 constexpr int kDecTiles = 16;  // key tiles of a CTA
 constexpr int kDecStages = 6;  // K chunks in flight
 constexpr int kDecThreads = 192;  // producer, MMA and 4 epilogue warps
@@ -694,7 +709,7 @@ struct DecCfg {
 };
 
 struct __align__(16) DecShared {
-  float nl2[kCols];
+  float nl2[kCols];  // of a column
   float sink[kCols];
   uint64_t q_full;
   uint64_t k_full[kDecStages], k_empty[kDecStages];
@@ -707,23 +722,71 @@ struct __align__(16) DecShared {
 template <int NCH, bool PAGED>
 __global__ void __launch_bounds__(kDecThreads)
     key_weights_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                              const KwParams p, const int n, const int tmem_cols) {
+                              const KwParams p, const int max_rows, const int n, const int tmem_cols) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
   uint8_t* sQ = smem + kDecStages * kChunkBytes;
+  // Base and range interval of a column's row, and the last first token it sees
+  // (more than one row: the columns are few).
+  int4* sV = reinterpret_cast<int4*>(sQ + NCH * n * 128);
+  int* sF = reinterpret_cast<int*>(sV + kFewCols);
   __shared__ DecShared sb;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   const int b = blockIdx.z, h = blockIdx.y;
   const Req r = load_req<PAGED>(p, b);
-  if (r.q_len != 1) return;
+  // All requests of the call have at most max_rows rows, or it is one and the
+  // others are left to the prefill kernel.
+  if (max_rows == 1 ? r.q_len != 1 : r.q_len < 1 && p.accumulate) return;
+  const int rows = min(r.q_len, max_rows), ncol = rows * p.group;
   const int key_lo = blockIdx.x * (kDecTiles * kKeys);
   if (key_lo >= r.k_len) return;
   const int tiles = min(kDecTiles, (r.k_len - key_lo + kKeys - 1) / kKeys);
-  const RowVis vis = row_visibility(p.m, r.ctx, r.k_len, table_active(p.m), r.q0, b);
-  const int f_hi = p.m.first_tokens > 0 ? first_tokens_hi(p.m, r.ctx, r.k_len) : -1;
-  auto meets = [&](int i) {  // the row sees a key of tile i
+  // The hulls of what the rows see, and the keys that all of them do; each
+  // column's own for the tiles between.
+  const bool use_table = table_active(p.m);
+  RowVis vis;
+  int f_hi = -1, all_lo, all_hi;
+  if (max_rows == 1) {
+    vis = row_visibility(p.m, r.ctx, r.k_len, use_table, r.q0, b);
+    if (p.m.first_tokens > 0) f_hi = first_tokens_hi(p.m, r.ctx, r.k_len);
+    all_lo = vis.b_lo;
+    all_hi = vis.b_hi;
+  } else {
+    vis.b_lo = vis.r_lo = INT_MAX;
+    vis.b_hi = vis.r_hi = -1;
+    all_lo = 0;
+    all_hi = rows > 0 ? r.k_len - 1 : -1;
+    for (int c = lane; c < ncol; c += 32) {
+      const int i = c / p.group;
+      const RowVis v = row_visibility(p.m, r.ctx + i, r.k_len, use_table, r.q0 + i, b);
+      const int f = p.m.first_tokens > 0 ? first_tokens_hi(p.m, r.ctx + i, r.k_len) : -1;
+      if (!v.base_empty()) {
+        vis.b_lo = min(vis.b_lo, v.b_lo);
+        vis.b_hi = max(vis.b_hi, v.b_hi);
+      }
+      if (!v.range_empty()) {
+        vis.r_lo = min(vis.r_lo, v.r_lo);
+        vis.r_hi = max(vis.r_hi, v.r_hi);
+      }
+      f_hi = max(f_hi, f);
+      all_lo = max(all_lo, v.b_lo);
+      all_hi = min(all_hi, v.b_hi);
+      if (warp == 0) {
+        sV[c] = make_int4(v.b_lo, v.b_hi, v.r_lo, v.r_hi);
+        sF[c] = f;
+      }
+    }
+    vis.b_lo = __reduce_min_sync(kFull, vis.b_lo);
+    vis.b_hi = __reduce_max_sync(kFull, vis.b_hi);
+    vis.r_lo = __reduce_min_sync(kFull, vis.r_lo);
+    vis.r_hi = __reduce_max_sync(kFull, vis.r_hi);
+    f_hi = __reduce_max_sync(kFull, f_hi);
+    all_lo = __reduce_max_sync(kFull, all_lo);
+    all_hi = __reduce_min_sync(kFull, all_hi);
+  }
+  auto meets = [&](int i) {  // a row may see a key of tile i
     const int a = key_lo + i * kKeys, e = a + kKeys - 1;
     return max(a, vis.b_lo) <= min(e, vis.b_hi) || max(a, vis.r_lo) <= min(e, vis.r_hi) || a <= f_hi;
   };
@@ -746,9 +809,12 @@ __global__ void __launch_bounds__(kDecThreads)
     tmem_alloc(&sb.tmem_base, tmem_cols);
     tmem_relinquish();
   }
-  for (int g = threadIdx.x; g < p.group; g += kDecThreads) {
-    sb.nl2[g] = -kLog2e * __ldg(p.lse + static_cast<size_t>(h * p.group + g) * p.m.total_q + r.q0);
-    sb.sink[g] = p.m.sink_mode == 1 && p.m.sinks != nullptr ? __ldg(p.m.sinks + h * p.group + g) * kLog2e : 0.f;
+  for (int c = threadIdx.x; c < ncol; c += kDecThreads) {
+    const int i = max_rows == 1 ? 0 : c / p.group, g = c - i * p.group;
+    sb.nl2[c] = in_bounds(r.q0 + i, p.m.total_q, p.err)
+                    ? -kLog2e * __ldg(p.lse + static_cast<size_t>(h * p.group + g) * p.m.total_q + r.q0 + i)
+                    : -INFINITY;
+    sb.sink[c] = p.m.sink_mode == 1 && p.m.sinks != nullptr ? __ldg(p.m.sinks + h * p.group + g) * kLog2e : 0.f;
   }
   tc_fence_before();
   __syncthreads();
@@ -760,7 +826,7 @@ __global__ void __launch_bounds__(kDecThreads)
       bool ok = true;
       int c = 0;
       const int run = PAGED ? min(kKeys, 1 << p.m.block_shift) : kKeys;
-      mbar_arrive_expect_tx(&sb.q_full, static_cast<uint32_t>(NCH * p.group * 128));
+      mbar_arrive_expect_tx(&sb.q_full, static_cast<uint32_t>(NCH * max_rows * p.group * 128));
       for (int x = 0; x < NCH; ++x) tma_load_3d(sQ + x * n * 128, &map_q, &sb.q_full, x * 64, h * p.group, r.q0);
       // Cache rows of a tile's runs (paged), looked up a tile ahead: the block
       // ids' latency is then not in the way of a freed stage.
@@ -858,21 +924,37 @@ __global__ void __launch_bounds__(kDecThreads)
         ok = mbar_wait(&sb.s_full[j & 1], (j >> 1) & 1, &sb.wc, p.err, kDevTimeoutMma);
         if (!ok) break;
         tc_fence_after();
-        const bool see = key < r.k_len && (vis.visible(key) || key <= f_hi);
-        for (int n0 = 0; n0 < n; n0 += 16) {
+        const int a = key_lo + i * kKeys;
+        const bool whole = a >= all_lo && a + kKeys - 1 <= all_hi;  // by all rows
+        const bool one = vis.visible(key) || key <= f_hi;           // (one row: its own intervals)
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int n0 = 0; n0 < ncol; n0 += 16) {
           uint32_t s[16];
           tmem_ld_32x32b_x16(base + (j & 1) * n + n0, s);
           tmem_ld_wait16(s);
+          if (whole && a > 0 && n0 + 16 <= ncol) {  // every key is seen, and none is key 0
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            if (n0 + q < p.group) {
-              float v = fmaf(__uint_as_float(s[q]), p.m.scale_log2, sb.nl2[n0 + q]);
-              if (key == 0) v += sb.sink[n0 + q];
-              total += ex2_approx(v);
+            for (int q = 0; q < 16; ++q)
+              sum[q & 3] += ex2_approx(fmaf(__uint_as_float(s[q]), p.m.scale_log2, sb.nl2[n0 + q]));
+            continue;
+          }
+          uint32_t seen = n0 + 16 <= ncol ? 0xffffu : (1u << (ncol - n0)) - 1u;
+          if (!whole && max_rows == 1) seen = one ? seen : 0u;
+          if (!whole && max_rows > 1) {
+#pragma unroll 4
+            for (int q = 0; q < min(16, ncol - n0); ++q) {
+              const int4 x = sV[n0 + q];
+              if (!((key >= x.x && key <= x.y) || (key >= x.z && key <= x.w) || key <= sF[n0 + q])) seen &= ~(1u << q);
             }
           }
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float nl2 = sb.nl2[n0 + q] + (key == 0 ? sb.sink[n0 + q] : 0.f);
+            const float e = ex2_approx(fmaf(__uint_as_float(s[q]), p.m.scale_log2, nl2));
+            sum[q & 3] += (seen >> q) & 1u ? e : 0.f;
+          }
         }
-        if (!see) total = 0.f;
+        total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sb.s_empty[j & 1]);
@@ -929,17 +1011,19 @@ cudaError_t launch_prefill_rows(const KwParams& p, const CUtensorMap& mq, const 
 }
 
 template <int NCH, bool PAGED>
-cudaError_t launch_decode_rows(const KwParams& p, int reqs, const CUtensorMap& mq, const CUtensorMap& mk,
+cudaError_t launch_decode_rows(const KwParams& p, int reqs, int rows, const CUtensorMap& mq, const CUtensorMap& mk,
                                cudaStream_t stream) {
   static bool done[64] = {};
-  constexpr int kMost = kDecStages * kChunkBytes + NCH * kCols * 128 + 1024;
+  constexpr int kFewBytes = kFewCols * 20;
+  constexpr int kMost = kDecStages * kChunkBytes + NCH * kCols * 128 + 1024 + (NCH < 8 ? kFewBytes : 0);
+  static_assert(NCH < 8 || kFewBytes <= NCH * (kCols / 4) * 128, "D = 512: it has the room of a quarter of the columns");
   cudaError_t e = set_smem(key_weights_decode_kernel<NCH, PAGED>, kMost, done);
   if (e != cudaSuccess) return e;
-  const int n = (p.group + 15) / 16 * 16;
+  const int n = (rows * p.group + 15) / 16 * 16;
   int cols = 32;
   while (cols < 2 * n) cols *= 2;
-  const int smem = kDecStages * kChunkBytes + NCH * n * 128 + 1024;
-  key_weights_decode_kernel<NCH, PAGED><<<dim3(p.n_kb, p.hkv, reqs), kDecThreads, smem, stream>>>(mq, mk, p, n, cols);
+  const int smem = kDecStages * kChunkBytes + NCH * n * 128 + 1024 + (rows > 1 ? kFewBytes : 0);
+  key_weights_decode_kernel<NCH, PAGED><<<dim3(p.n_kb, p.hkv, reqs), kDecThreads, smem, stream>>>(mq, mk, p, rows, n, cols);
   return cudaGetLastError();
 }
 
@@ -1029,8 +1113,14 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
   // (unless rows are padding): the prefill kernel takes them all, right for
   // single tokens too, and the other one is not launched.
   const bool no_single = num_decode_reqs < 0 && total_q > static_cast<long long>(num_reqs - 1) * max_q_len + 1;
-  const int decode_count = no_single ? 0 : (num_decode_reqs < 0 ? num_reqs : num_decode_reqs);
-  const int first = num_decode_reqs < 0 ? 0 : num_decode_reqs;
+  // No request of more than a few rows: the single tokens' kernel takes them
+  // all, with a column per row and head (up to its 128, 33 rows of 4 heads take
+  // 839 us in the other one and 32 rows 402 here; 96 at D = 512, where 33 rows
+  // of 4 take 264 and 24 take 143).
+  const bool few = max_q_len > 1 && max_q_len * static_cast<long long>(num_heads_q / num_heads_kv) <= (head_dim == 512 ? kFewCols * 3 / 4 : kFewCols);  // (what shared memory holds)
+  const int decode_count = few ? num_reqs : no_single ? 0 : (num_decode_reqs < 0 ? num_reqs : num_decode_reqs);
+  const int first = few ? num_reqs : num_decode_reqs < 0 ? 0 : num_decode_reqs;
+  const int dec_rows = few ? max_q_len : 1;
   // Requests without queries (q_len 0) are set to 0 by the prefill kernel.
   const bool run_prefill = first < num_reqs && (max_q_len > 1 || !accumulate);
   const int box = paged ? std::min(kKeys, 1 << block_shift) : kKeys;
@@ -1042,7 +1132,7 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
     if (!encode_bf16_3d(&mq, q, head_dim, num_heads_q, total_q, 64, p.group, p.npos, true)) return MVP_ERR_UNSUPPORTED;
     KwParams pp = p;
     pp.req_offset = first;
-    pp.skip_decode = no_single ? 0 : 1;
+    pp.skip_decode = no_single || num_decode_reqs >= 0 ? 0 : 1;  // (only where the other kernel covers them too)
     pp.n_kb = (max_k_len + kTile - 1) / kTile;
     pp.splits = split_count(num_reqs - first, p.hkv, max_q_len, max_k_len, p.npos, num_sms);
     const size_t one = static_cast<size_t>(num_reqs) * p.hkv * pp.n_kb * kTile * sizeof(float);
@@ -1081,15 +1171,15 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
     }
   }
   if (decode_count > 0) {
-    if (!encode_bf16_3d(&mq, q, head_dim, num_heads_q, total_q, 64, p.group, 1, true)) return MVP_ERR_UNSUPPORTED;
+    if (!encode_bf16_3d(&mq, q, head_dim, num_heads_q, total_q, 64, p.group, dec_rows, true)) return MVP_ERR_UNSUPPORTED;
     KwParams pd = p;
     pd.n_kb = (max_k_len + kDecTiles * kKeys - 1) / (kDecTiles * kKeys);
     cudaError_t e = cudaErrorInvalidValue;
     switch (head_dim) {
-      case 64: e = paged ? launch_decode_rows<1, true>(pd, decode_count, mq, mk, st) : launch_decode_rows<1, false>(pd, decode_count, mq, mk, st); break;
-      case 128: e = paged ? launch_decode_rows<2, true>(pd, decode_count, mq, mk, st) : launch_decode_rows<2, false>(pd, decode_count, mq, mk, st); break;
-      case 256: e = paged ? launch_decode_rows<4, true>(pd, decode_count, mq, mk, st) : launch_decode_rows<4, false>(pd, decode_count, mq, mk, st); break;
-      case 512: e = paged ? launch_decode_rows<8, true>(pd, decode_count, mq, mk, st) : launch_decode_rows<8, false>(pd, decode_count, mq, mk, st); break;
+      case 64: e = paged ? launch_decode_rows<1, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<1, false>(pd, decode_count, dec_rows, mq, mk, st); break;
+      case 128: e = paged ? launch_decode_rows<2, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<2, false>(pd, decode_count, dec_rows, mq, mk, st); break;
+      case 256: e = paged ? launch_decode_rows<4, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<4, false>(pd, decode_count, dec_rows, mq, mk, st); break;
+      case 512: e = paged ? launch_decode_rows<8, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<8, false>(pd, decode_count, dec_rows, mq, mk, st); break;
     }
     if (e != cudaSuccess) return MVP_ERR_CUDA;
     ++launches;

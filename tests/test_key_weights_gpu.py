@@ -133,6 +133,17 @@ def test_single_tokens(d, hq, hkv, window, first):
     assert torch.equal(a, Case(w, first).run(n_dec=6))
 
 
+@pytest.mark.parametrize("d,hq,hkv,q", [(64, 4, 4, [3, 64, 0, 17]), (128, 8, 1, [8, 1, 5, 2]), (256, 12, 4, [21, 20, 1, 0]),
+                                        (512, 32, 1, [2, 1, 2, 0]), (64, 6, 2, [22, 3, 1, 1]),
+                                        (128, 4, 4, [128, 1, 39, 2]), (512, 8, 2, [24, 2, 0, 1]), (64, 3, 1, [43, 43, 1, 9])])
+@pytest.mark.parametrize("window,first,ranges", [(-1, 0, False), (60, 9, False), (900, 0, True), (3, 200, True)])
+def test_few_rows(d, hq, hkv, q, window, first, ranges):
+    """Up to 128 columns (rows x heads of a KV head; 96 at D = 512) go through the single
+    tokens' kernel, and the next size through the other one."""
+    w = _w(q, [2300, 64, 40, 900], hq, hkv, d, window, sink=1, seed=d + hq)
+    Case(w, first, _table(w, d) if ranges else None).check_all(32, n_dec=0 if ranges else -1)
+
+
 @pytest.mark.parametrize("d", [64, 256])
 @pytest.mark.parametrize("q,k", [([130, 300], [400, 301]), ([1, 1], [300, 2])])
 def test_key0_sinks_far_apart(d, q, k, monkeypatch):
