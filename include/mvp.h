@@ -310,9 +310,12 @@ int mvp_attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
  * (tokens, not the per-head sink logits, which combine with them as with any
  * other mask).  As in the plain calls, V of a masked key that shares a 128-key
  * tile with a visible one must be finite (it is multiplied by a probability of
- * zero); K of masked keys may hold anything.  first_tokens >= 0; 0, or window_left = -1, is the plain call
- * bit for bit.  The key tiles between the first tokens and the window are
- * never read.  All other arguments, results and errors are those of the plain
+ * zero); K of masked keys may hold anything.  first_tokens >= 0; 0, or
+ * window_left = -1, is the plain call bit for bit.  The key tiles between the
+ * first tokens and the window are never read.  While SMs would have no work,
+ * single-token rows are split into parts of as few as 256 keys, as far as the
+ * workspace holds their partials (mvp_attn_workspace_size gives room for one
+ * part per 4096 keys; a larger workspace allows more).  All other arguments, results and errors are those of the plain
  * calls; MVP_ERR_ARG also for first_tokens < 0.
  */
 int mvp_attn_fwd_varlen_first(const void* q, const void* k, const void* v, void* out, float* lse,

@@ -110,6 +110,7 @@ int largest_pow2_divisor(int g, int cap) {
 }
 
 constexpr int kDecodeChunk = 4096;
+constexpr int kFirstChunk = 256;  // with first tokens, of few rows (see below)
 constexpr int kMaxSplits = 64;
 
 }  // namespace
@@ -399,6 +400,15 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
       span = std::min(span, window_left + static_cast<long long>(kt) + first);
     }
     int splits = static_cast<int>((span + kDecodeChunk - 1) / kDecodeChunk);
+    const int per_cta = decode_heads_per_cta(head_dim, group);
+    const long long head_ctas = static_cast<long long>(num_heads_kv) * ((group + per_cta - 1) / per_cta);
+    // With first tokens the walks are short (a window and a few tiles): split
+    // further while the GPU has SMs without a CTA, down to kFirstChunk keys, as
+    // far as the workspace goes.  3 requests of up to 21339 keys, 16/8 heads, D =
+    // 512, a window of 1389 and 51 first tokens: 90 us, 144 in one part; 7 of up
+    // to 5066, D = 256, window 2622: 84 and 138.
+    if (m.first_tokens > 0 && decode_count > 0)
+      splits = static_cast<int>(std::max<long long>(splits, std::min(num_sms / (decode_count * head_ctas), span / kFirstChunk)));
     if (splits > kMaxSplits) splits = kMaxSplits;
     const size_t per_split = static_cast<size_t>(decode_count) * num_heads_q * (head_dim + 2) * sizeof(float);
     if (partials == nullptr) splits = 1;
@@ -411,8 +421,7 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
     dp.n_splits = splits;
     dp.chunk = static_cast<int>(chunk);
     dp.partial = splits > 1 ? static_cast<float*>(partials) : nullptr;
-    const int per_cta = decode_heads_per_cta(head_dim, group);
-    if (static_cast<long long>(num_heads_kv) * ((group + per_cta - 1) / per_cta) > 65535) return MVP_ERR_UNSUPPORTED;
+    if (head_ctas > 65535) return MVP_ERR_UNSUPPORTED;
     const int box = decode_box_inner(head_dim);
     if (!encode_3d(&dmk, k, head_dim, num_heads_kv, total_k, box, 1, box_rows(kt), false) ||
         !encode_3d(&dmv, v, head_dim, num_heads_kv, total_k, box, 1, box_rows(kt), false))

@@ -3,6 +3,8 @@
 the other attention tests (``gpu_helpers.compare``: 1e-2 or two bf16 half
 steps of the value, lse 1e-3 relative)."""
 
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -98,6 +100,15 @@ def test_decode(d, hq, hkv, first, window):
     x, a = _check(w, first, 128, ws=False)
     b = _packed(w, x, first, n_dec=5)
     gh.compare(*b, a[0].double().cpu().numpy(), a[1].double().cpu().numpy(), what="split", strict=False)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 1), (128, 8, 2), (256, 4, 2), (512, 2, 1)])
+@pytest.mark.parametrize("first,window", [(4, 1000), (300, 3000), (9000, 5)])
+def test_few_rows_in_many_parts(d, hq, hkv, first, window, monkeypatch):
+    """A workspace with room for 30 parts of a row, more than keys per 4096."""
+    monkeypatch.setattr(sys.modules[__name__], "_ws", lambda w, n_dec=-1: torch.empty(
+        mvp.attn_workspace_size(w.num_reqs, hq, d, 30 * 4096), dtype=torch.uint8, device="cuda"))
+    _check(_w([1] * 3, [9001, 700, 1], hq, hkv, d, window, sink=first % 3, seed=d + first), first, 64)
 
 
 @pytest.mark.parametrize("seed", range(10))
