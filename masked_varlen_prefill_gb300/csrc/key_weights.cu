@@ -703,11 +703,6 @@ constexpr int kDecTiles = 16;  // key tiles of a CTA
 constexpr int kDecStages = 6;  // K chunks in flight
 constexpr int kDecThreads = 192;  // producer, MMA and 4 epilogue warps
 
-template <int NCH>
-struct DecCfg {
-  static constexpr int Q_BYTES(int n) { return NCH * n * 128; }
-};
-
 struct __align__(16) DecShared {
   float nl2[kCols];  // of a column
   float sink[kCols];
