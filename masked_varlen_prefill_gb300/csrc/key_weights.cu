@@ -1112,7 +1112,8 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
   // all, with a column per row and head (up to its 128, 33 rows of 4 heads take
   // 839 us in the other one and 32 rows 402 here; 96 at D = 512, where 33 rows
   // of 4 take 264 and 24 take 143).
-  const bool few = max_q_len > 1 && max_q_len * static_cast<long long>(num_heads_q / num_heads_kv) <= (head_dim == 512 ? kFewCols * 3 / 4 : kFewCols);  // (what shared memory holds)
+  const int most = head_dim == 512 ? kFewCols * 3 / 4 : kFewCols;  // (what shared memory holds)
+  const bool few = max_q_len > 1 && static_cast<long long>(max_q_len) * p.group <= most;
   const int decode_count = few ? num_reqs : no_single ? 0 : (num_decode_reqs < 0 ? num_reqs : num_decode_reqs);
   const int first = few ? num_reqs : num_decode_reqs < 0 ? 0 : num_decode_reqs;
   const int dec_rows = few ? max_q_len : 1;
@@ -1150,10 +1151,22 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
     if (2 * pairs > INT_MAX) return MVP_ERR_UNSUPPORTED;
     cudaError_t e = cudaErrorInvalidValue;
     switch (head_dim) {
-      case 64: e = paged ? launch_prefill_rows<1, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<1, false>(pp, mq, mk, pairs, st); break;
-      case 128: e = paged ? launch_prefill_rows<2, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<2, false>(pp, mq, mk, pairs, st); break;
-      case 256: e = paged ? launch_prefill_rows<4, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<4, false>(pp, mq, mk, pairs, st); break;
-      case 512: e = paged ? launch_prefill_rows<8, true>(pp, mq, mk, pairs, st) : launch_prefill_rows<8, false>(pp, mq, mk, pairs, st); break;
+      case 64:
+        e = paged ? launch_prefill_rows<1, true>(pp, mq, mk, pairs, st)
+                  : launch_prefill_rows<1, false>(pp, mq, mk, pairs, st);
+        break;
+      case 128:
+        e = paged ? launch_prefill_rows<2, true>(pp, mq, mk, pairs, st)
+                  : launch_prefill_rows<2, false>(pp, mq, mk, pairs, st);
+        break;
+      case 256:
+        e = paged ? launch_prefill_rows<4, true>(pp, mq, mk, pairs, st)
+                  : launch_prefill_rows<4, false>(pp, mq, mk, pairs, st);
+        break;
+      case 512:
+        e = paged ? launch_prefill_rows<8, true>(pp, mq, mk, pairs, st)
+                  : launch_prefill_rows<8, false>(pp, mq, mk, pairs, st);
+        break;
     }
     if (e != cudaSuccess) return MVP_ERR_CUDA;
     ++launches;
@@ -1171,10 +1184,22 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
     pd.n_kb = (max_k_len + kDecTiles * kKeys - 1) / (kDecTiles * kKeys);
     cudaError_t e = cudaErrorInvalidValue;
     switch (head_dim) {
-      case 64: e = paged ? launch_decode_rows<1, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<1, false>(pd, decode_count, dec_rows, mq, mk, st); break;
-      case 128: e = paged ? launch_decode_rows<2, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<2, false>(pd, decode_count, dec_rows, mq, mk, st); break;
-      case 256: e = paged ? launch_decode_rows<4, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<4, false>(pd, decode_count, dec_rows, mq, mk, st); break;
-      case 512: e = paged ? launch_decode_rows<8, true>(pd, decode_count, dec_rows, mq, mk, st) : launch_decode_rows<8, false>(pd, decode_count, dec_rows, mq, mk, st); break;
+      case 64:
+        e = paged ? launch_decode_rows<1, true>(pd, decode_count, dec_rows, mq, mk, st)
+                  : launch_decode_rows<1, false>(pd, decode_count, dec_rows, mq, mk, st);
+        break;
+      case 128:
+        e = paged ? launch_decode_rows<2, true>(pd, decode_count, dec_rows, mq, mk, st)
+                  : launch_decode_rows<2, false>(pd, decode_count, dec_rows, mq, mk, st);
+        break;
+      case 256:
+        e = paged ? launch_decode_rows<4, true>(pd, decode_count, dec_rows, mq, mk, st)
+                  : launch_decode_rows<4, false>(pd, decode_count, dec_rows, mq, mk, st);
+        break;
+      case 512:
+        e = paged ? launch_decode_rows<8, true>(pd, decode_count, dec_rows, mq, mk, st)
+                  : launch_decode_rows<8, false>(pd, decode_count, dec_rows, mq, mk, st);
+        break;
     }
     if (e != cudaSuccess) return MVP_ERR_CUDA;
     ++launches;
