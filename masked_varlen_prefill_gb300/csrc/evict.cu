@@ -15,8 +15,8 @@
 //    through distributed shared memory.  It reads 4 bytes of each key's
 //    weight (from L2 after the first time), against 4 * D bytes of K and V
 //    that the move reads and writes for a kept one.  Bound by its instructions
-//    (about 40 per 32 keys) and by what a pass costs whatever the keys (1500
-//    cycles; 900 instructions per warp in all): 48 requests of 4096 to 32768
+//    (about 40 per 32 keys) and by the latency of a pass whatever the keys (1500
+//    cycles between its barriers): 48 requests of 4096 to 32768
 //    keys, 8 KV heads, 40 us (four compares and a prefix sum per key in place
 //    of the votes, and always three passes: 50).
 // 2. evict_move_kernel copies the kept rows, 32 KB per CTA, all of it in flight
