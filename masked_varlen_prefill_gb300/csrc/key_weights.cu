@@ -1106,8 +1106,10 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
 
   // Mixed in any order, but so many rows that every request has more than one
   // (unless rows are padding): the prefill kernel takes them all, right for
-  // single tokens too, and the other one is not launched.
-  const bool no_single = num_decode_reqs < 0 && total_q > static_cast<long long>(num_reqs - 1) * max_q_len + 1;
+  // single tokens too, and the other one is not launched.  (Not where no request
+  // has more than one: there all rows past the requests' are padding.)
+  const bool no_single =
+      num_decode_reqs < 0 && max_q_len > 1 && total_q > static_cast<long long>(num_reqs - 1) * max_q_len + 1;
   // No request of more than a few rows: the single tokens' kernel takes them
   // all, with a column per row and head (up to its 128, 33 rows of 4 heads take
   // 839 us in the other one and 32 rows 402 here; 96 at D = 512, where 33 rows

@@ -310,3 +310,26 @@ def test_refused_in_python():
                dict(weights=torch.zeros((1, 2, 9), dtype=torch.float64, device="cuda"))):
         with pytest.raises(ValueError):
             c.run(**kw)
+
+
+@pytest.mark.parametrize("q,k", [([1] * 5, [300, 40, 17, 2700, 1]), ([1, 0, 1, 0], [300, 40, 17, 5])])
+@pytest.mark.parametrize("accumulate", [True, False])
+@pytest.mark.parametrize("block", [0, 16])
+def test_padded_single_tokens(q, k, accumulate, block):
+    """A decode step of fewer requests than its rows have room for."""
+    w = _w(q, k, 4, 2, 128, 90, seed=len(q))
+    c = Case(w, 3)
+    rows = 8
+    qp = torch.full((rows, 4, 128), float("nan"), dtype=torch.bfloat16, device=c.dev)
+    qp[:w.total_q] = c.x[0]
+    lse = torch.full((4, rows), float("nan"), device=c.dev)
+    lse[:, :w.total_q] = torch.tensor(c.lse, device=c.dev)
+    out = torch.tensor(c.w0, device=c.dev)
+    kw = dict(window_left=90, first_tokens=3, scale=w.scale, accumulate=accumulate)
+    if block:
+        kc, _, bt, sl = workloads.to_paged(c.x[1], c.x[2], k, block, seed=1, table_fill=-5)
+        mvp.attn_key_weights_paged(qp, kc, lse, out, c.t32(c.cu_q), sl, bt, block, 1, c.max_k, **kw)
+    else:
+        mvp.attn_key_weights_varlen(qp, c.x[1], lse, out, c.t32(c.cu_q), c.t32(c.cu_k), 1, c.max_k, **kw)
+    assert mvp.last_launch_count() > 0
+    c.check(out, accumulate)
