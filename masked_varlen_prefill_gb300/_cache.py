@@ -57,13 +57,18 @@ def _call(fn_name, dev, stream, *args):
 
 
 def _caches(k_cache, v_cache, block_size):
-    """The caches as [rows, Hkv, D] and their number of blocks."""
+    """The caches as [rows, Hkv, D], views of the caller's memory, and their
+    number of blocks."""
     shape = k_cache.shape
     if v_cache.shape != shape:
         raise ValueError("the caches differ in shape")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches must be contiguous")
     if len(shape) == 4:
-        k_cache = k_cache.reshape(-1, *shape[2:])
-        v_cache = v_cache.reshape(-1, *shape[2:])
+        if shape[1] != block_size:
+            raise ValueError(f"the caches' blocks have {shape[1]} rows, not block_size ({block_size})")
+        k_cache = k_cache.view(-1, *shape[2:])
+        v_cache = v_cache.view(-1, *shape[2:])
         shape = k_cache.shape
     if len(shape) != 3:
         raise ValueError("the caches must be [num_blocks * block_size, Hkv, D]")
@@ -124,8 +129,9 @@ def rope_append_paged(q, k, v, q_out, k_cache, v_cache, positions, table, cu_seq
     ``attn_fwd_paged`` with the same offsets and block table.
 
     q [total_q, Hq, D], k/v [total_q, Hkv, D] bf16 or fp32, rows any stride
-    (views of one projection); q_out bf16 like q, contiguous; positions int32
-    [num_axes, total_q]; table a ``RopeTable``.
+    (views of one projection); q_out bf16 like q, contiguous; the caches
+    [num_blocks * block_size, Hkv, D] or [num_blocks, block_size, Hkv, D],
+    contiguous; positions int32 [num_axes, total_q]; table a ``RopeTable``.
     """
     dev = _cuda_device(q_out, "q_out")
     block_size = int(block_size)
@@ -217,8 +223,8 @@ def attn_key_weights_paged(q, k_cache, lse, weights, cu_seqlens_q, seq_lens_k, b
                            max_k_len, *, slots=None, context_lens=None, range_table=None, range_covered=None,
                            causal=True, window_left=-1, window_right=-1, first_tokens=0, sinks=None, sink_mode=0,
                            scale=None, accumulate=True, workspace=None, num_decode_reqs=-1, stream=None):
-    """``attn_key_weights_varlen`` over a paged cache: the weights of the
-    ``attn_fwd_paged`` call with these arguments."""
+    """``attn_key_weights_varlen`` over a paged cache (contiguous): the weights
+    of the ``attn_fwd_paged`` call with these arguments."""
     dev = _cuda_device(q, "q")
     block_size = int(block_size)
     k_cache, _, num_blocks = _caches(k_cache, k_cache, block_size)
@@ -254,10 +260,12 @@ def kv_evict_paged(k_cache, v_cache, weights, seq_lens_k, block_table, block_siz
     weights, keeping the first and the most recent ones (see
     ``mvp_kv_evict_paged`` in include/mvp.h).
 
-    weights fp32 [num_slots, Hkv, max_len]; new_seq_lens int32 [B] and kept
-    int32 [B, Hkv, budget] are written; workspace uint8 of
-    ``kv_evict_workspace_size(B, Hkv, budget)`` bytes.  In place unless
-    ``block_table_out`` / ``weights_out`` say where the kept keys go.
+    The caches are [num_blocks * block_size, Hkv, D] or [num_blocks,
+    block_size, Hkv, D], contiguous; weights fp32 [num_slots, Hkv, max_len];
+    new_seq_lens int32 [B] and kept int32 [B, Hkv, budget] are written;
+    workspace uint8 of ``kv_evict_workspace_size(B, Hkv, budget)`` bytes.  In
+    place unless ``block_table_out`` / ``weights_out`` say where the kept keys
+    go.
     """
     dev = _cuda_device(k_cache, "k_cache")
     block_size, budget = int(block_size), int(budget)

@@ -221,3 +221,36 @@ def test_key_weights_refusals(lib):
         assert call(True, **over) == mvp.MVP_ERR_ARG, over
     assert mvp.key_weights_workspace_size(0, 1, 1, 1) == 0
     assert mvp.key_weights_workspace_size(4, 8, 1, 10000) == 0  # single tokens need none
+
+
+# ------------------------------------------------------------------ caches of four dimensions
+def test_caches_are_written_where_they_are():
+    """[num_blocks, block_size, Hkv, D] caches are viewed as rows, never
+    copied: what a call writes there would be lost with the copy."""
+    import torch
+
+    from masked_varlen_prefill_gb300._cache import _caches
+
+    k, v = torch.zeros(4, 16, 2, 64), torch.zeros(4, 16, 2, 64)
+    a, b, blocks = _caches(k, v, 16)
+    assert blocks == 4 and a.shape == (64, 2, 64)
+    assert a.data_ptr() == k.data_ptr() and b.data_ptr() == v.data_ptr()
+    both = torch.zeros(4, 2, 16, 2, 64)  # K and V of a block next to each other
+    for pair in ((both[:, 0], both[:, 1]), (k, both[:, 1]), (both[:, 0], v), (k.transpose(1, 2), v.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            _caches(*pair, 16)
+    two = torch.zeros(2, 4, 16, 2, 64)  # one tensor, K and V apart
+    a, b, _ = _caches(two[0], two[1], 16)
+    assert a.data_ptr() == two.data_ptr() and b.data_ptr() == two[1].data_ptr()
+
+
+def test_block_size_of_a_cache_of_four_dimensions():
+    import torch
+
+    from masked_varlen_prefill_gb300._cache import _caches
+
+    k = torch.zeros(4, 32, 2, 64)
+    for block in (16, 64, 0):
+        with pytest.raises(ValueError):
+            _caches(k, k, block)
+    assert _caches(k, k, 32)[2] == 4

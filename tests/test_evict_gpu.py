@@ -182,3 +182,26 @@ def test_refused_in_python():
         c.run()
     with pytest.raises(mvp.MvpError):
         Case([300], 1, 64, 16, 100).run(ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_caches_of_four_dimensions():
+    c = Case([300, 70], 2, 64, 16, 64, 4, 10, seed=9)
+    ref = c.run()
+    c.check(ref)
+    t32 = lambda x: torch.tensor(x, dtype=torch.int32, device=c.dev)  # noqa: E731
+
+    def call(k, v):
+        w, new = torch.tensor(c.w0, device=c.dev), t32([0, 0])
+        kept = torch.zeros((2, 2, 64), dtype=torch.int32, device=c.dev)
+        ws = torch.empty(mvp.kv_evict_workspace_size(2, 2, 64), dtype=torch.uint8, device=c.dev)
+        mvp.kv_evict_paged(k, v, w, t32(c.lens), t32(c.bt), 16, 64, new, kept, ws, c.max_k, first_tokens=4,
+                           recent_tokens=10)
+        return w
+
+    shape = (-1, 16, 2, 64)
+    k, v = c.k0.clone(), c.v0.clone()
+    assert torch.equal(call(k.view(shape), v.view(shape)), ref[2])
+    assert torch.equal(k, ref[0]) and torch.equal(v, ref[1])
+    both = torch.stack([c.k0.view(shape), c.v0.view(shape)], 1)  # K and V of a block next to each other
+    with pytest.raises(ValueError):
+        call(both[:, 0], both[:, 1])

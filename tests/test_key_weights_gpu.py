@@ -333,3 +333,21 @@ def test_padded_single_tokens(q, k, accumulate, block):
         mvp.attn_key_weights_varlen(qp, c.x[1], lse, out, c.t32(c.cu_q), c.t32(c.cu_k), 1, c.max_k, **kw)
     assert mvp.last_launch_count() > 0
     c.check(out, accumulate)
+
+
+def test_caches_of_four_dimensions():
+    c = Case(_w([40, 1], [60, 300], 4, 2, 64, seed=5))
+    kc, _, bt, sl = workloads.to_paged(c.x[1], c.x[2], c.w.k_lens, 16, seed=2, table_fill=-5)
+    lse = torch.tensor(c.lse, device=c.dev)
+
+    def call(cache):
+        out = torch.tensor(c.w0, device=c.dev)
+        mvp.attn_key_weights_paged(c.x[0], cache, lse, out, c.t32(c.cu_q), sl, bt, 16, 40, c.max_k, scale=c.w.scale)
+        return out
+
+    a = call(kc)
+    c.check(a)
+    blocks = kc.view(-1, 16, 2, 64)
+    assert torch.equal(a, call(blocks))
+    with pytest.raises(ValueError):
+        call(torch.stack([blocks, blocks], 1)[:, 0])

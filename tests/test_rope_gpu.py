@@ -201,3 +201,17 @@ def test_far_rows_of_a_large_cache():
     torch.cuda.synchronize()
     assert torch.equal(q_out, ref[0]) and torch.equal(big[shift * 256:], ref[1]) and torch.equal(vc[shift * 256:], ref[2])
     assert not big[:shift * 256].any()
+
+
+def test_caches_of_four_dimensions():
+    c = _case([40, 3], [60, 3], 4, 2, 64, 64, 2, 16, torch.bfloat16, False, seed=21)
+    ref = _run(c)
+    _check(c, *ref)
+    shape = (-1, 16, 2, 64)
+    kc, vc = c["k0"].clone(), c["v0"].clone()
+    q_out = torch.full(c["q"].shape, 7.0, dtype=torch.bfloat16, device=kc.device)
+    mvp.rope_append_paged(c["q"], c["k"], c["v"], q_out, kc.view(shape), vc.view(shape), *c["args"])
+    assert torch.equal(kc, ref[1]) and torch.equal(vc, ref[2])
+    both = torch.stack([c["k0"].view(shape), c["v0"].view(shape)], 1)  # K and V of a block next to each other
+    with pytest.raises(ValueError):
+        mvp.rope_append_paged(c["q"], c["k"], c["v"], q_out, both[:, 0], both[:, 1], *c["args"])
