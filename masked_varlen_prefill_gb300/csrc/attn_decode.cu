@@ -114,8 +114,13 @@ __device__ __forceinline__ int row_off(int kk, int lane) {
 }
 
 // PAGED: K/V rows come through a block table (compile-time, so the packed
-// kernel carries none of the paged addressing).
-template <int D, int GP, bool PAGED>
+// kernel carries none of the paged addressing).  FIRST: the window leaves
+// first tokens visible (compile-time too: their walk costs registers, and the
+// paged D = 128 form with four heads has none to spare: at more than 128 only
+// two of its CTAs fit an SM instead of three, and 256 rows under a 4096-key
+// window take 674 us instead of 635, 512 rows of 100 .. 400 keys 136 instead of
+// 109).
+template <int D, int GP, bool PAGED, bool FIRST>
 __global__ void __launch_bounds__(DCfg<D>::THREADS)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const DecodeParams p) {
@@ -169,15 +174,17 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
   // First tokens that stay visible: the tiles that hold them come before the
   // hull's in the row's walk (n_first keys, whole tiles, none of the hull's).
   // The walk's w-th key is key w of those, then key lo + w - n_first.
-  const int f_hi = p.m.first_tokens > 0 ? first_tokens_hi(p.m, pos, k_len) : -1;
-  if (f_hi >= 0 && lo > hi) {  // nothing but first tokens
+  int f_hi = -1;
+  if constexpr (FIRST) f_hi = first_tokens_hi(p.m, pos, k_len);
+  if (FIRST && f_hi >= 0 && lo > hi) {  // nothing but first tokens
     lo = (f_hi + C::KT) & ~(C::KT - 1);
     hi = lo - 1;
   }
-  const int n_first = f_hi >= 0 ? min((f_hi + C::KT) & ~(C::KT - 1), lo) : 0;
+  const int n_first = FIRST && f_hi >= 0 ? min((f_hi + C::KT) & ~(C::KT - 1), lo) : 0;
   const int skip = lo - n_first;  // keys between the first tokens' tiles and the hull's
   const int n_walk = (lo <= hi || n_first > 0) ? n_first + (hi - lo + 1) : 0;
   const int w_lo = sp * p.chunk;
+  // (without first tokens n_first = 0: the walk is the hull's)
   const int n_keys = max(0, min(n_walk - w_lo, p.chunk));
   const int n_tiles = (n_keys + C::KT - 1) / C::KT;
   const bool single = p.partial == nullptr;
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
       // not in the way of a freed stage.
       auto key_of = [&](int t) {
         const int w0 = w_lo + t * C::KT;
-        return w0 < n_first ? w0 : w0 + skip;
+        return FIRST && w0 < n_first ? w0 : w0 + skip;
       };
       constexpr int kRuns = PAGED ? C::KT / 16 : 1;
       int next[kRuns];
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
     const uint8_t* ks_tile = smem + s * 2 * C::TILE;
     const uint8_t* vs_tile = ks_tile + C::TILE;
     const int w0 = w_lo + t * C::KT;
-    const int t0 = w0 < n_first ? w0 : w0 + skip;
+    const int t0 = FIRST && w0 < n_first ? w0 : w0 + skip;
     const bool interior = t0 >= core_lo && t0 + C::KT - 1 <= core_hi;
     for (int gi = warp; gi < NG; gi += C::NW) {
       float x[NSUB];
@@ -394,7 +401,7 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
         if (!interior) {
           const int key = t0 + kk;
           if (key0_mode && key == 0) x[a] += my_sink;
-          if (!vis.visible(key) && key > f_hi) x[a] = -INFINITY;
+          if (!vis.visible(key) && !(FIRST && key <= f_hi)) x[a] = -INFINITY;
         }
       }
       // max of head hh over the step's keys: this lane's NSUB, then the KS keys
@@ -563,10 +570,10 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeParams 
 // device at the same time).
 std::mutex g_decode_attr_mutex;
 
-template <int D, int GP>
+template <int D, int GP, bool FIRST>
 cudaError_t launch_dg(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
   const bool paged = p.m.block_table != nullptr;
-  auto kern = paged ? attn_decode_kernel<D, GP, true> : attn_decode_kernel<D, GP, false>;
+  auto kern = paged ? attn_decode_kernel<D, GP, true, FIRST> : attn_decode_kernel<D, GP, false, FIRST>;
   static bool attr_set[2][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -586,16 +593,16 @@ cudaError_t launch_dg(const DecodeParams& p, const CUtensorMap& mk, const CUtens
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool FIRST>
 cudaError_t launch_d(const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream,
                      int* launches) {
   // Heads per CTA: the group padded to a power of two, capped so that q and
   // the accumulators (2 * GP * D / 32 floats per lane) stay in registers.
   cudaError_t e;
-  if (p.group == 1) e = launch_dg<D, 1>(p, mk, mv, stream);
-  else if (p.group == 2) e = launch_dg<D, 2>(p, mk, mv, stream);
-  else if (p.group <= 4 || D >= 512) e = launch_dg<D, 4>(p, mk, mv, stream);
-  else if constexpr (D < 512) e = launch_dg<D, 8>(p, mk, mv, stream);
+  if (p.group == 1) e = launch_dg<D, 1, FIRST>(p, mk, mv, stream);
+  else if (p.group == 2) e = launch_dg<D, 2, FIRST>(p, mk, mv, stream);
+  else if (p.group <= 4 || D >= 512) e = launch_dg<D, 4, FIRST>(p, mk, mv, stream);
+  else if constexpr (D < 512) e = launch_dg<D, 8, FIRST>(p, mk, mv, stream);
   else e = cudaErrorInvalidValue;
   if (e != cudaSuccess) return e;
   ++*launches;
@@ -609,6 +616,18 @@ cudaError_t launch_d(const DecodeParams& p, const CUtensorMap& mk, const CUtenso
   return cudaSuccess;
 }
 
+template <bool FIRST>
+cudaError_t launch_decode_dim(int head_dim, const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                              cudaStream_t stream, int* launches) {
+  switch (head_dim) {
+    case 64: return launch_d<64, FIRST>(p, mk, mv, stream, launches);
+    case 128: return launch_d<128, FIRST>(p, mk, mv, stream, launches);
+    case 256: return launch_d<256, FIRST>(p, mk, mv, stream, launches);
+    case 512: return launch_d<512, FIRST>(p, mk, mv, stream, launches);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 }  // namespace
 
 int decode_keys_per_tile(int head_dim) { return kt_for(head_dim); }
@@ -616,13 +635,8 @@ int decode_box_inner(int head_dim) { return box_for(head_dim); }
 
 cudaError_t launch_decode(int head_dim, const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
                           cudaStream_t stream, int* launches) {
-  switch (head_dim) {
-    case 64: return launch_d<64>(p, mk, mv, stream, launches);
-    case 128: return launch_d<128>(p, mk, mv, stream, launches);
-    case 256: return launch_d<256>(p, mk, mv, stream, launches);
-    case 512: return launch_d<512>(p, mk, mv, stream, launches);
-    default: return cudaErrorInvalidValue;
-  }
+  return p.m.first_tokens > 0 ? launch_decode_dim<true>(head_dim, p, mk, mv, stream, launches)
+                              : launch_decode_dim<false>(head_dim, p, mk, mv, stream, launches);
 }
 
 }  // namespace mvp

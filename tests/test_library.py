@@ -185,3 +185,21 @@ def test_binding_has_no_cpu_path():
             if f.endswith((".py", ".cu", ".cuh", ".h", ".cpp")):
                 src = open(os.path.join(dirpath, f)).read()
                 assert "import oracle" not in src and "from oracle" not in src, f
+
+
+def test_decode_kernels_keep_three_ctas_per_sm(lib):
+    """The D = 128 decode kernels for up to four heads per KV head have two
+    ring stages so that three CTAs fit an SM: 5 warps each, 65536 registers,
+    so at most 128 per thread (without first tokens; see attn_decode.cu)."""
+    from masked_varlen_prefill_gb300 import _build
+
+    log = os.path.join(_build.OBJDIR, "ptxas.log")
+    if not os.path.exists(log):
+        _build.build()
+    used = {}
+    for entry in open(log).read().split("Compiling entry function")[1:]:
+        name = re.search(r"attn_decode_kernelILi128ELi([124])ELb([01])E(?:Lb0E)?EEv", entry.split("\n")[0])
+        if name:
+            used[name.group(1), name.group(2)] = int(re.search(r"Used (\d+) registers", entry).group(1))
+    assert len(used) == 6, used
+    assert max(used.values()) <= 128, used
