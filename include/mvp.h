@@ -606,7 +606,8 @@ int mvp_rope_table_pack(const double* inv_freq, const int32_t* axes, int pairs, 
  * which is the column sum of the probabilities of the attention call that
  * wrote lse (same masks, sinks and scale; null-logit sinks enter through lse
  * alone).  Keys that a row does not see, or that nothing sees, add 0 whatever
- * they hold.  The sums are fp32 and the same in every run.
+ * they hold, and so does a row and head whose lse is -inf (it has no
+ * probabilities).  The sums are fp32 and the same in every run.
  *
  * q, k (k_cache), cu_seqlens_q .. num_decode_reqs, masks, sinks, scale: as in
  *               mvp_attn_fwd_varlen_first / mvp_attn_fwd_paged_first.

@@ -510,8 +510,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!__all_sync(kFull, ok)) break;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          // an infinite lse: a weight of zero (or, of -inf, infinity) whatever the score
-          const float v = fabsf(l[k]) == INFINITY ? copysignf(kHuge, -l[k]) : (l[k] - base) * inv;
+          // an infinite lse: a weight of zero whatever the score (of -inf too: its
+          // row has no probabilities, whether it sees nothing or a key that a sink
+          // of -inf closes)
+          const float v = fabsf(l[k]) == INFINITY ? -kHuge : (l[k] - base) * inv;
           const float hi = bf16(v), mid = bf16(v - hi);
           const uint32_t w0 = pack_bf16x2(hi, mid), w1 = pack_bf16x2((v - hi) - mid, 0.f);
           *reinterpret_cast<uint4*>(sE + (2 + es) * kExtBytes + 16 * (lane + 32 * k)) =
@@ -806,9 +808,10 @@ __global__ void __launch_bounds__(kDecThreads)
   }
   for (int c = threadIdx.x; c < ncol; c += kDecThreads) {
     const int i = max_rows == 1 ? 0 : c / p.group, g = c - i * p.group;
-    sb.nl2[c] = in_bounds(r.q0 + i, p.m.total_q, p.err)
-                    ? -kLog2e * __ldg(p.lse + static_cast<size_t>(h * p.group + g) * p.m.total_q + r.q0 + i)
-                    : -INFINITY;
+    const float l = in_bounds(r.q0 + i, p.m.total_q, p.err)
+                        ? __ldg(p.lse + static_cast<size_t>(h * p.group + g) * p.m.total_q + r.q0 + i)
+                        : INFINITY;
+    sb.nl2[c] = l == -INFINITY ? l : -kLog2e * l;  // (a row without probabilities: 0)
     sb.sink[c] = p.m.sink_mode == 1 && p.m.sinks != nullptr ? __ldg(p.m.sinks + h * p.group + g) * kLog2e : 0.f;
   }
   tc_fence_before();

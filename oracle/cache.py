@@ -68,13 +68,16 @@ def attend(q, k, v, mask, scale, sinks=None, sink_mode=0):
 
 def key_weights(q, k, lse, mask, scale, sinks=None, sink_mode=0):
     """One request: w [Hkv, k_len], the sum over the rows that see a key and
-    over the query heads of its KV head of exp(score - lse)."""
+    over the query heads of its KV head of exp(score - lse).  A row whose lse
+    is -inf has no probabilities (it sees nothing, or only scores of -inf)."""
     hq, hkv = q.shape[1], k.shape[1]
     w = np.zeros((hkv, k.shape[0]))
     for h in range(hq):
         s = _scores(q, k, h, hq // hkv, scale, sinks, sink_mode)
-        e = np.exp(np.where(mask, s - np.asarray(lse, dtype=np.float64)[h][:, None], -np.inf))
-        w[h // (hq // hkv)] += np.where(mask, e, 0.0).sum(axis=0)
+        z = np.asarray(lse, dtype=np.float64)[h][:, None]
+        seen = mask & (z > -np.inf)
+        e = np.exp(np.where(seen, s - np.where(z > -np.inf, z, 0.0), -np.inf))
+        w[h // (hq // hkv)] += np.where(seen, e, 0.0).sum(axis=0)
     return w
 
 

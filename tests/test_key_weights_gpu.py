@@ -351,3 +351,28 @@ def test_caches_of_four_dimensions():
     assert torch.equal(a, call(blocks))
     with pytest.raises(ValueError):
         call(torch.stack([blocks, blocks], 1)[:, 0])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q,k", [([1, 1], [1, 40]), ([130, 300], [130, 300]), ([3, 5], [3, 7])])
+def test_rows_whose_only_key_a_sink_closes(q, k, d, monkeypatch):
+    """A key-0 sink of -inf and a row that sees no other key: its scores are
+    all -inf, its lse too, and it gives key 0 nothing."""
+    inputs = gh.make_inputs
+
+    def closed(w):
+        x = inputs(w)
+        x[3].copy_(torch.tensor([-np.inf, 0.5, -np.inf, -1.0]))
+        return x
+
+    monkeypatch.setattr(gh, "make_inputs", closed)
+    w = _w(q, k, 4, 2, d, sink=1, seed=d)
+    c = Case(w)
+    assert np.isneginf(c.lse[[0, 2], 0]).all() and np.isfinite(c.add).all()
+    c.check_all(16)
+    # ... as the attention call leaves it
+    lse = torch.empty((4, w.total_q), device=c.dev)
+    out = torch.empty_like(c.x[0])
+    mvp.attn_fwd_varlen(c.x[0], c.x[1], c.x[2], out, c.t32(c.cu_q), c.t32(c.cu_k), max(q), max(k), lse=lse,
+                        sinks=c.x[3], sink_mode=1, scale=w.scale)
+    assert torch.isneginf(lse[[0, 2], 0]).all() and (out[0, [0, 2]] == 0).all()
