@@ -80,13 +80,22 @@ struct Eight {
   float x[8];
 };
 
+// 16 bytes of q, k or v, by an ordinary load: q_out may be q, and the read-only
+// path is for memory that nothing writes during the kernel.  (Each 16 bytes are
+// read and written by one thread, so loads need no order among the stores.)
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
+}
+
 // Eight elements as they lie in memory, and their values.
 template <class T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = ld16(p); }
   __device__ __forceinline__ Eight get() const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     Eight e;
@@ -100,12 +109,15 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
-  float4 a, b;
+  uint4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = ld16(p);
+    b = ld16(p + 4);
   }
-  __device__ __forceinline__ Eight get() const { return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+  __device__ __forceinline__ Eight get() const {
+    return {{__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+             __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)}};
+  }
 };
 
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const Eight& e) {

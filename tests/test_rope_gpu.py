@@ -215,3 +215,18 @@ def test_caches_of_four_dimensions():
     both = torch.stack([c["k0"].view(shape), c["v0"].view(shape)], 1)  # K and V of a block next to each other
     with pytest.raises(ValueError):
         mvp.rope_append_paged(c["q"], c["k"], c["v"], q_out, both[:, 0], both[:, 1], *c["args"])
+
+
+@pytest.mark.parametrize("rows,hq,d,rot", [(50, 40, 256, 64), (50, 64, 128, 128), (4000, 2, 64, 32)])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_queries_in_place_of_many_heads(rows, hq, d, rot, adjacent):
+    """A thread takes several pieces of a row in turn, some after others of
+    that row were written, and (4000 rows) a CTA several rows."""
+    c = _case([rows - 3, 3], [rows, 30], hq, 2, d, rot, 2, 16, torch.bfloat16, adjacent, seed=rows + hq, fused=False)
+    before = c["q"].clone()
+    ref = _run(c)
+    q_out, kc, vc = _run(c, q_out=c["q"])
+    torch.cuda.synchronize()
+    assert torch.equal(q_out, ref[0]) and torch.equal(kc, ref[1]) and torch.equal(vc, ref[2])
+    c["q"] = before
+    _check(c, q_out, kc, vc)
