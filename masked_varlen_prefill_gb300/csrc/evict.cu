@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(kMoveThreads, 5) evict_move_kernel(const Evict
     }
   }
   if (!__all_sync(0xffffffffu, ok)) return;
+  __syncwarp();  // what one lane acquired holds for the other lanes' stores (a vote does not order memory)
 #pragma unroll
   for (int u = 0; u < kMoveChunks; ++u) {
     const int i = row_of(u);
