@@ -215,9 +215,9 @@ def fill_query_ranges(ranges, query_start_loc, seq_lens, out, num_tokens, rows_w
     max_ranges = 0 if ranges is None else ranges.shape[1]
     if ranges is not None and (ranges.dim() != 3 or ranges.shape[0] != num_reqs or ranges.shape[2] != 2):
         raise ValueError("ranges must be [num_reqs, max_ranges, 2]")
-    st = lib.mvp_fill_query_ranges(_ptr(ranges), num_reqs, max_ranges, _ptr(query_start_loc), _ptr(seq_lens),
-                                   int(num_tokens), _ptr(out), out.shape[0], _ptr(rows_written),
-                                   _stream(stream, dev))
+    st = _on(dev, lib.mvp_fill_query_ranges,
+             (_ptr(ranges), num_reqs, max_ranges, _ptr(query_start_loc), _ptr(seq_lens), int(num_tokens), _ptr(out),
+              out.shape[0], _ptr(rows_written), _stream(stream, dev)))
     if st != MVP_OK:
         raise MvpError("mvp_fill_query_ranges", st)
 
@@ -276,7 +276,7 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
         name, st = "mvp_attn_fwd_varlen", _on(dev, lib.mvp_attn_fwd_varlen, args)
     else:
         opts = AttnOptions(int(variant), int(wait_limit_us), int(fault), int(mixed_prefill_sms))
-        name, st = "mvp_attn_fwd_varlen_ext", lib.mvp_attn_fwd_varlen_ext(*args, ctypes.byref(opts))
+        name, st = "mvp_attn_fwd_varlen_ext", _on(dev, lib.mvp_attn_fwd_varlen_ext, (*args, ctypes.byref(opts)))
     if st != MVP_OK:
         raise MvpError(name, st)
 
@@ -310,11 +310,11 @@ def attn_fwd_varlen_scan(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, ma
     if scale is None:
         scale = d ** -0.5
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib.mvp_attn_fwd_varlen_scan(
+    st = _on(dev, lib.mvp_attn_fwd_varlen_scan, (
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
         _ptr(context_lens), num_reqs, total_q, total_k, int(max_q_len), int(max_k_len), int(num_decode_reqs),
         hq, hkv, d, _ptr(ranges), max_ranges, int(bool(causal)), int(window_left), int(window_right),
-        _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes, _stream(stream, dev))
+        _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes, _stream(stream, dev)))
     if st != MVP_OK:
         raise MvpError("mvp_attn_fwd_varlen_scan", st)
 
@@ -390,11 +390,11 @@ def attn_fwd_varlen_static_ws(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_le
     total_k, hkv, _ = k.shape
     if scale is None:
         scale = d ** -0.5
-    st = lib.mvp_attn_fwd_varlen_static_ws(
+    st = _on(dev, lib.mvp_attn_fwd_varlen_static_ws, (
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
         _ptr(context_lens), cu_seqlens_q.shape[0] - 1, total_q, total_k, int(max_q_len), int(max_k_len),
         int(num_decode_reqs), hq, hkv, d, _ptr(range_table), _ptr(range_covered), int(bool(causal)),
-        int(window_left), int(window_right), _ptr(sinks), int(sink_mode), float(scale), _stream(stream, dev))
+        int(window_left), int(window_right), _ptr(sinks), int(sink_mode), float(scale), _stream(stream, dev)))
     if st != MVP_OK:
         raise MvpError("mvp_attn_fwd_varlen_static_ws", st)
 
@@ -424,10 +424,11 @@ def attn_fwd_varlen_host(q, k, v, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
 
 
 def get_last_device_error(stream=None) -> int:
-    """Synchronise and return (and clear) the library's device error status."""
+    """Synchronise and return (and clear) the library's device error status of
+    the stream's device (default: the current one)."""
     lib = load_library()
-    dev = torch.device("cuda", torch.cuda.current_device())
-    return int(lib.mvp_get_last_device_error(_stream(stream, dev)))
+    dev = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
+    return int(_on(dev, lib.mvp_get_last_device_error, (_stream(stream, dev),)))
 
 
 def last_launch_count() -> int:
@@ -536,7 +537,7 @@ class StepMetadata:
 
     def upload(self, stream=None):
         """Copy the staged block to the device and fill the range table."""
-        st = self._lib.mvp_meta_upload(self._handle, _stream(stream, self.device))
+        st = _on(self.device, self._lib.mvp_meta_upload, (self._handle, _stream(stream, self.device)))
         if st != MVP_OK:
             raise MvpError("mvp_meta_upload", st)
 
