@@ -319,20 +319,30 @@ def attn_fwd_varlen_scan(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, ma
         raise MvpError("mvp_attn_fwd_varlen_scan", st)
 
 
+def _rows_of_blocks(cache, stream):
+    """A cache [num_blocks, block_size, Hkv, D] as rows.  Blocks that lie apart
+    are copied, on the stream that reads them (and to its memory)."""
+    shape = (-1, *cache.shape[2:])
+    if cache.is_contiguous():
+        return cache.view(shape)
+    with torch.cuda.stream(stream):
+        return cache.reshape(shape)
+
+
 def attn_fwd_paged(q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_table, block_size, max_q_len,
                    max_k_len, *, lse=None, context_lens=None, range_table=None, range_covered=None, causal=True,
                    window_left=-1, window_right=-1, sinks=None, sink_mode=SINK_NONE, scale=None, workspace=None,
                    num_decode_reqs=-1, stream=None, first_tokens=0):
     """Masked varlen attention over a paged K/V cache (see
     ``mvp_attn_fwd_paged``): k_cache/v_cache [num_blocks * block_size, Hkv,
-    D] (or [num_blocks, block_size, Hkv, D]) bf16, block_table int32 [B,
+    D] (or [num_blocks, block_size, Hkv, D], copied in each call unless
+    contiguous) bf16, block_table int32 [B,
     max_blocks_per_seq], seq_lens_k int32 [B]; the rest as ``attn_fwd_varlen``
     (``first_tokens``: ``mvp_attn_fwd_paged_first``)."""
     lib = load_library()
     dev = q.device
     if k_cache.dim() == 4:
-        k_cache = k_cache.reshape(-1, k_cache.shape[2], k_cache.shape[3])
-        v_cache = v_cache.reshape(-1, v_cache.shape[2], v_cache.shape[3])
+        k_cache, v_cache = _rows_of_blocks(k_cache, stream), _rows_of_blocks(v_cache, stream)
     for n, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
         _check_cuda(n, t, torch.bfloat16, dev)
     for n, t in (("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k), ("block_table", block_table),

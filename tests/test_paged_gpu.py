@@ -90,3 +90,22 @@ def test_decode_first_paged():
     while n_dec < w.num_reqs and w.q_lens[n_dec] == 1:
         n_dec += 1
     _paged_parity(w, 16, num_decode_reqs=n_dec, strict=True)
+
+
+def test_interleaved_cache_on_another_stream():
+    """A cache whose K and V blocks alternate is flattened on the stream the
+    attention runs on, not beside it."""
+    w = workloads.Workload("interleaved", 7, [40, 1], [700, 900], 4, 2, 64, True, -1, 0, 0, None)
+    q, k, v, sinks = gh.make_inputs(w)
+    ref, _, (kc, vc, bt, sl) = _run_paged(w, q, k, v, sinks, 16, None, None)
+    both = torch.stack([kc.view(-1, 16, 2, 64), vc.view(-1, 16, 2, 64)], 1)
+    cu_q, _ = gh.device_meta(w, q.device)
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        out = torch.zeros_like(q)
+        torch.full((2, *kc.shape), 5.0, dtype=torch.bfloat16, device=q.device)  # (freed: what a copy may land in)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)  # the current stream is busy, the side stream is not
+        mvp.attn_fwd_paged(q, both[:, 0], both[:, 1], out, cu_q, sl, bt, 16, 40, 900, scale=w.scale, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
