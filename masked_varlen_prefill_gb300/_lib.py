@@ -174,9 +174,10 @@ def _ptr(t):
 
 def _stream(stream, device):
     if stream is None:
-        if device.index is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (not of torch's public interface)
+        if raw is None or device.index is None:
             return torch.cuda.current_stream(device).cuda_stream
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return raw(device.index)
     return stream.cuda_stream
 
 

@@ -151,3 +151,14 @@ def test_the_error_word_is_that_of_the_streams_device(calls):
     mvp.get_last_device_error()
     mvp.get_last_device_error(Stream())
     assert calls == [("mvp_get_last_device_error", 0, (100,)), ("mvp_get_last_device_error", 1, (777,))]
+
+
+def test_the_current_stream_by_the_public_interface(calls, monkeypatch):
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+
+    class Stream:
+        cuda_stream = 555
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: Stream() if dev == DEV else None)
+    mvp.attn_fwd_varlen(*_packed())
+    assert calls[0][:2] == ("mvp_attn_fwd_varlen", 1) and 555 in calls[0][2]
