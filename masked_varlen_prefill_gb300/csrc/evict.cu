@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     if (cl > 1) cluster_sync_all();
     else __syncthreads();
   };
-  griddep_wait();
   if (c == 0) {
     for (int i = tid; i < p.n_segs; i += kSelThreads) p.flags[static_cast<size_t>(bh) * p.n_segs + i] = 0;
     if (bh == 0 && tid == 0) *p.ticket = 0;

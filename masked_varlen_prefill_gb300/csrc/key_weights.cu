@@ -71,7 +71,7 @@ struct KwParams {
   int num_slots;
   long long w_stride;
   int accumulate;
-  int num_reqs, hq, hkv, group;
+  int num_reqs, hkv, group;
   int req_offset;          // prefill kernel: first request it covers
   int skip_decode;         // prefill kernel: leave single-token requests
   int npos;                // query positions per tile
@@ -265,7 +265,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
 
-  griddep_wait();
   int x = blockIdx.x >> 1;
   const int n_groups = (p.n_kb + p.blocks - 1) / p.blocks;
   const bool grouped = x < p.grouped_rows * n_groups;
@@ -686,7 +685,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 // Adds the splits' partial sums up, in their order.
 template <bool PAGED>
 __global__ void __launch_bounds__(256) key_weights_combine_kernel(const KwParams p) {
-  griddep_wait();
   const int h = blockIdx.y, b = blockIdx.z + p.req_offset;
   const Req r = load_req<PAGED>(p, b);
   if (p.skip_decode && r.q_len == 1) return;
@@ -730,7 +728,6 @@ __global__ void __launch_bounds__(kDecThreads)
   int* sF = reinterpret_cast<int*>(sV + kFewCols);
   __shared__ DecShared sb;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  griddep_wait();
   const int b = blockIdx.z, h = blockIdx.y;
   const Req r = load_req<PAGED>(p, b);
   // All requests of the call have at most max_rows rows, or it is one and the
@@ -1100,7 +1097,6 @@ int key_weights_impl(const void* q, const void* k, const float* lse, float* weig
   p.w_stride = weight_stride;
   p.accumulate = accumulate;
   p.num_reqs = num_reqs;
-  p.hq = num_heads_q;
   p.hkv = num_heads_kv;
   p.group = num_heads_q / num_heads_kv;
   p.npos = kCols / p.group;

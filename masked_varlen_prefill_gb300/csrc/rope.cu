@@ -10,9 +10,9 @@
 // tokens half an ulp of the product is 0.03 radians), so the table holds
 // each frequency as turns per position, f / 2 pi, in 64-bit fixed point: the
 // product with the position wraps modulo one turn by itself, exactly, and its
-// upper 32 bits are the turn within 2^-32.  sincospi of twice that turn is
-// correct to fp32 at every int32 position.  Rotation is in fp32, rounded once
-// to bf16 (what the attention kernels read).
+// upper 32 bits are the turn within 2^-32.  It is then rounded to fp32: an angle
+// within 1e-7 radians at every int32 position, as fine as the fp32 rotation,
+// which is rounded once to bf16 (what the attention kernels read).
 //
 // The kernel is bound by memory: (Hq + 2 Hkv) * D elements of each token are
 // read and written once.  A CTA takes one token (up to eight small ones): a few
@@ -137,8 +137,7 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 && !MANY ? 10 : 6
   const int mine = MANY ? static_cast<int>(threadIdx.x) / group : 0;
   const int tid = MANY ? static_cast<int>(threadIdx.x) % group : static_cast<int>(threadIdx.x);
   const int t0 = blockIdx.x * tokens, t = MANY ? min(t0 + mine, p.total_q - 1) : t0;
-  griddep_launch_dependents();
-  griddep_wait();
+  griddep_launch_dependents();  // (an attention call behind this one sets up beside it)
   const T* q = static_cast<const T*>(p.q) + static_cast<size_t>(t) * p.q_stride;
   const T* k = static_cast<const T*>(p.k) + static_cast<size_t>(t) * p.k_stride;
   const T* v = static_cast<const T*>(p.v) + static_cast<size_t>(t) * p.v_stride;
