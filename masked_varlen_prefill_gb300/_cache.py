@@ -14,7 +14,7 @@ import ctypes
 import numpy as np
 import torch
 
-from ._lib import MVP_OK, MvpError, _on, _stream, load_library
+from ._lib import MVP_OK, MvpError, _on, _rows_of_blocks, _stream, load_library
 
 _I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 
@@ -223,10 +223,12 @@ def attn_key_weights_paged(q, k_cache, lse, weights, cu_seqlens_q, seq_lens_k, b
                            max_k_len, *, slots=None, context_lens=None, range_table=None, range_covered=None,
                            causal=True, window_left=-1, window_right=-1, first_tokens=0, sinks=None, sink_mode=0,
                            scale=None, accumulate=True, workspace=None, num_decode_reqs=-1, stream=None):
-    """``attn_key_weights_varlen`` over a paged cache (contiguous): the weights
-    of the ``attn_fwd_paged`` call with these arguments."""
+    """``attn_key_weights_varlen`` over a paged cache: the weights of the
+    ``attn_fwd_paged`` call with these arguments."""
     dev = _cuda_device(q, "q")
     block_size = int(block_size)
+    if len(k_cache.shape) == 4 and k_cache.shape[1] == block_size:
+        k_cache = _rows_of_blocks(k_cache, stream)
     k_cache, _, num_blocks = _caches(k_cache, k_cache, block_size)
     _need(dev, _I32, "seq_lens_k", seq_lens_k, "block_table", block_table)
     num_reqs = seq_lens_k.shape[0]

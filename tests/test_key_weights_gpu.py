@@ -349,8 +349,20 @@ def test_caches_of_four_dimensions():
     c.check(a)
     blocks = kc.view(-1, 16, 2, 64)
     assert torch.equal(a, call(blocks))
+    # K next to V in each block: read from a copy, as the attention call does, on the call's stream
+    both = torch.stack([blocks, torch.full_like(blocks, 3.0)], 1)
+    assert torch.equal(a, call(both[:, 0]))
+    side = torch.cuda.Stream()
+    torch.full((2, *kc.shape), 5.0, dtype=torch.bfloat16, device=c.dev)
+    out = torch.tensor(c.w0, device=c.dev)
+    args = (lse, out, c.t32(c.cu_q), sl, bt, 16, 40, c.max_k)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)  # the current stream is busy, the side stream is not
+    mvp.attn_key_weights_paged(c.x[0], both[:, 0], *args, scale=c.w.scale, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(a, out)
     with pytest.raises(ValueError):
-        call(torch.stack([blocks, blocks], 1)[:, 0])
+        call(kc.view(-1, 32, 2, 64))
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
