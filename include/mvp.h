@@ -336,6 +336,77 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
                              size_t workspace_bytes, void* stream);
 
 /*
+ * mvp_attn_fwd_varlen_first / mvp_attn_fwd_paged_first with functions of the
+ * score and documents that do not see each other.  The score of query
+ * position p and key j in head h is
+ *   s = scale * q.k
+ *   s = softcap * tanh(s / softcap)         if softcap > 0
+ *   s = s - distance_slopes[h] * |p - j|    if distance_slopes is given
+ * (then the key-0 sink, where that mode is on: sinks are not capped), and key j
+ * is visible only if it also lies in the row's document,
+ *   visible = (base || rng || first) && doc_table[row][0] <= j <= doc_table[row][1]
+ * Documents narrow what the other masks leave: a range (a bidirectional
+ * prefix of each document, say) that reaches into another document ends where
+ * the document does, and first_tokens are the request's, seen by rows of the
+ * document that holds them.
+ *
+ * softcap         0 (no cap) or 1e-30 .. 1e30.
+ * distance_slopes fp32 [num_heads_q], any finite values, or NULL.  Distances
+ *                 up to 2^24 are exact.
+ * doc_table       int32 [total_q, 2], 8-byte aligned, or NULL: the closed key
+ *                 interval of each row's document (mvp_fill_query_documents).
+ *                 A row with an empty interval sees nothing (out = 0).  V of
+ *                 another document's key that shares a 128-key tile with a
+ *                 visible key must be finite, as for any masked key.
+ * scores          NULL, or with none of the three: the _first call, bit for
+ *                 bit.
+ * All other arguments, results and errors are those of the _first calls;
+ * MVP_ERR_ARG also for a softcap out of range or NaN,
+ * MVP_ERR_UNSUPPORTED for a doc_table that is not 8-byte aligned.
+ * mvp_attn_key_weights_* and mvp_attn_accounting know of none of these.
+ */
+typedef struct {
+  float softcap;                 /* 0: none */
+  const float* distance_slopes;  /* [num_heads_q] or NULL */
+  const int32_t* doc_table;      /* [total_q, 2] or NULL */
+} mvp_score_options;
+int mvp_attn_fwd_varlen_scored(const void* q, const void* k, const void* v, void* out, float* lse,
+                               const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, const int32_t* context_lens,
+                               int num_reqs, int total_q, int total_k, int max_q_len, int max_k_len,
+                               int num_decode_reqs, int num_heads_q, int num_heads_kv, int head_dim,
+                               const int32_t* range_table, const int32_t* range_covered, int causal, int window_left,
+                               int window_right, int first_tokens, const float* sinks, int sink_mode, float scale,
+                               void* workspace, size_t workspace_bytes, void* stream, const mvp_score_options* scores);
+int mvp_attn_fwd_paged_scored(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                              const int32_t* cu_seqlens_q, const int32_t* seq_lens_k, const int32_t* block_table,
+                              int block_size, int max_blocks_per_seq, int num_blocks, const int32_t* context_lens,
+                              int num_reqs, int total_q, int max_q_len, int max_k_len, int num_decode_reqs,
+                              int num_heads_q, int num_heads_kv, int head_dim, const int32_t* range_table,
+                              const int32_t* range_covered, int causal, int window_left, int window_right,
+                              int first_tokens, const float* sinks, int sink_mode, float scale, void* workspace,
+                              size_t workspace_bytes, void* stream, const mvp_score_options* scores);
+
+/*
+ * The documents of mvp_attn_fwd_*_scored as a table, the counterpart of
+ * mvp_fill_query_ranges: packed query row t of request b, at absolute position
+ * p = seq_lens[b] - q_len + (t - query_start_loc[b]), gets the closed interval
+ * [last start <= p, next start - 1] of the request's documents.
+ *
+ * doc_starts      int32 [num_reqs, max_docs], ascending: the positions at which
+ *                 documents start.  Positions before the first form a document
+ *                 of their own (a start at 0 may be left out); a start of
+ *                 INT_MAX is padding, and the last document ends at
+ *                 INT_MAX - 1.
+ * query_start_loc, seq_lens, num_tokens, out, out_capacity: as in
+ *                 mvp_fill_query_ranges; rows at or past
+ *                 query_start_loc[num_reqs] are written as (-1, -1).
+ * Errors: MVP_ERR_ARG, MVP_ERR_CAPACITY, MVP_ERR_UNSUPPORTED (out not 8-byte
+ * aligned), MVP_ERR_CUDA.  num_tokens == 0: nothing is launched.
+ */
+int mvp_fill_query_documents(const int32_t* doc_starts, int num_reqs, int max_docs, const int32_t* query_start_loc,
+                             const int32_t* seq_lens, int num_tokens, int32_t* out, int out_capacity, void* stream);
+
+/*
  * Scan mode: the same attention with the request-level range list of vLLM's
  * Triton path instead of the per-row table (PR #50294 review,
  * "Implementation breakdown" 2: the (num_seqs, max_ranges, 2) tensor that

@@ -34,6 +34,7 @@ from ._lib import (  # noqa: F401
     attn_fwd_varlen_static_ws,
     attn_workspace_size,
     bounds_checked,
+    fill_query_documents,
     fill_query_ranges,
     get_last_device_error,
     last_launch_count,

@@ -55,6 +55,12 @@ class AttnCounts(ctypes.Structure):
                 ("decode_read_bytes", ctypes.c_double), ("decode_cta_read_bytes", ctypes.c_double)]
 
 
+class ScoreOptions(ctypes.Structure):
+    """``mvp_score_options`` (include/mvp.h)."""
+
+    _fields_ = [("softcap", ctypes.c_float), ("distance_slopes", ctypes.c_void_p), ("doc_table", ctypes.c_void_p)]
+
+
 class AttnOptions(ctypes.Structure):
     """``mvp_attn_options`` (include/mvp.h)."""
 
@@ -75,6 +81,13 @@ _SIGNATURES = {
                                        _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
     "mvp_attn_fwd_paged_first": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _i, _i, _i,
                                       _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp]),
+    "mvp_attn_fwd_varlen_scored": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                                        _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp,
+                                        ctypes.POINTER(ScoreOptions)]),
+    "mvp_attn_fwd_paged_scored": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _i, _i, _i,
+                                       _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _i, _f, _vp, _sz, _vp,
+                                       ctypes.POINTER(ScoreOptions)]),
+    "mvp_fill_query_documents": (_i, [_vp, _i, _i, _vp, _vp, _i, _vp, _i, _vp]),
     "mvp_attn_fwd_varlen_static_ws": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                            _i, _i, _vp, _vp, _i, _i, _i, _vp, _i, _f, _vp]),
     "mvp_static_scratch_bytes": (_sz, []),
@@ -223,6 +236,43 @@ def fill_query_ranges(ranges, query_start_loc, seq_lens, out, num_tokens, rows_w
         raise MvpError("mvp_fill_query_ranges", st)
 
 
+def fill_query_documents(doc_starts, query_start_loc, seq_lens, out, num_tokens, stream=None):
+    """Per-row document table (see ``mvp_fill_query_documents`` in
+    include/mvp.h): the ``doc_table`` of the attention calls.
+
+    doc_starts int32 [B, max_docs] ascending per request (INT_MAX: padding),
+    or None (one document per request); the rest as ``fill_query_ranges``.
+    """
+    lib = load_library()
+    dev = out.device
+    for n, t in (("doc_starts", doc_starts), ("query_start_loc", query_start_loc), ("seq_lens", seq_lens),
+                 ("out", out)):
+        _check_cuda(n, t, torch.int32, dev)
+    num_reqs = seq_lens.shape[0]
+    if doc_starts is not None and (doc_starts.dim() != 2 or doc_starts.shape[0] != num_reqs):
+        raise ValueError("doc_starts must be [num_reqs, max_docs]")
+    if query_start_loc.shape != (num_reqs + 1,) or out.dim() != 2 or out.shape[1] != 2:
+        raise ValueError("query_start_loc must be [B + 1] and out [capacity, 2]")
+    st = _on(dev, lib.mvp_fill_query_documents,
+             (_ptr(doc_starts), num_reqs, 0 if doc_starts is None else doc_starts.shape[1], _ptr(query_start_loc),
+              _ptr(seq_lens), int(num_tokens), _ptr(out), out.shape[0], _stream(stream, dev)))
+    if st != MVP_OK:
+        raise MvpError("mvp_fill_query_documents", st)
+
+
+def _score_options(softcap, distance_slopes, doc_table, num_heads_q, total_q, dev):
+    """``mvp_score_options`` of an attention call, or None when none is given."""
+    if softcap == 0 and distance_slopes is None and doc_table is None:
+        return None
+    _check_cuda("distance_slopes", distance_slopes, torch.float32, dev)
+    _check_cuda("doc_table", doc_table, torch.int32, dev)
+    if distance_slopes is not None and distance_slopes.shape != (num_heads_q,):
+        raise ValueError("distance_slopes must be [Hq]")
+    if doc_table is not None and doc_table.shape != (total_q, 2):
+        raise ValueError("doc_table must be [total_q, 2]")
+    return ctypes.byref(ScoreOptions(float(softcap), _ptr(distance_slopes), _ptr(doc_table)))
+
+
 def attn_workspace_size(num_reqs, num_heads_q, head_dim, max_k_len) -> int:
     return int(load_library().mvp_attn_workspace_size(num_reqs, num_heads_q, head_dim, max_k_len))
 
@@ -231,7 +281,8 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
                     context_lens=None, range_table=None, range_covered=None, causal=True, window_left=-1,
                     window_right=-1, sinks=None, sink_mode=SINK_NONE, scale=None, workspace=None,
                     num_decode_reqs=-1, stream=None, variant=VARIANT_DEFAULT, wait_limit_us=0,
-                    fault=FAULT_NONE, mixed_prefill_sms=0, first_tokens=0):
+                    fault=FAULT_NONE, mixed_prefill_sms=0, first_tokens=0, softcap=0.0, distance_slopes=None,
+                    doc_table=None):
     """Masked varlen attention forward (see ``mvp_attn_fwd_varlen``).
 
     q [total_q, Hq, D], k/v [total_k, Hkv, D] bf16; out like q; lse fp32
@@ -240,6 +291,10 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
     than their defaults go through ``mvp_attn_fwd_varlen_ext`` with those
     options.  ``first_tokens``: keys below it stay visible past
     ``window_left`` (``mvp_attn_fwd_varlen_first``; not with those options).
+    ``softcap`` / ``distance_slopes`` fp32 [Hq] / ``doc_table`` int32
+    [total_q, 2] (``fill_query_documents``): scores capped by a tanh, biased
+    by -slope |p - j|, and rows that see their document alone
+    (``mvp_attn_fwd_varlen_scored``; not with those options).
     """
     lib = load_library()
     dev = q.device
@@ -267,8 +322,15 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
             hq, hkv, d, _ptr(range_table), _ptr(range_covered), int(bool(causal)), int(window_left),
             int(window_right), _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes,
             _stream(stream, dev)]
+    scores = _score_options(softcap, distance_slopes, doc_table, hq, total_q, dev)
     plain = variant == VARIANT_DEFAULT and wait_limit_us == 0 and fault == FAULT_NONE and mixed_prefill_sms == 0
-    if first_tokens != 0:
+    if scores is not None:
+        if not plain:
+            raise ValueError("softcap, distance_slopes and doc_table do not combine with variant, wait_limit_us, fault "
+                             "or mixed_prefill_sms")
+        args.insert(22, int(first_tokens))
+        name, st = "mvp_attn_fwd_varlen_scored", _on(dev, lib.mvp_attn_fwd_varlen_scored, (*args, scores))
+    elif first_tokens != 0:
         if not plain:
             raise ValueError("first_tokens does not combine with variant, wait_limit_us, fault or mixed_prefill_sms")
         args.insert(22, int(first_tokens))
@@ -333,13 +395,15 @@ def _rows_of_blocks(cache, stream):
 def attn_fwd_paged(q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_table, block_size, max_q_len,
                    max_k_len, *, lse=None, context_lens=None, range_table=None, range_covered=None, causal=True,
                    window_left=-1, window_right=-1, sinks=None, sink_mode=SINK_NONE, scale=None, workspace=None,
-                   num_decode_reqs=-1, stream=None, first_tokens=0):
+                   num_decode_reqs=-1, stream=None, first_tokens=0, softcap=0.0, distance_slopes=None,
+                   doc_table=None):
     """Masked varlen attention over a paged K/V cache (see
     ``mvp_attn_fwd_paged``): k_cache/v_cache [num_blocks * block_size, Hkv,
     D] (or [num_blocks, block_size, Hkv, D], copied in each call unless
     contiguous) bf16, block_table int32 [B,
     max_blocks_per_seq], seq_lens_k int32 [B]; the rest as ``attn_fwd_varlen``
-    (``first_tokens``: ``mvp_attn_fwd_paged_first``)."""
+    (``first_tokens``: ``mvp_attn_fwd_paged_first``; ``softcap``,
+    ``distance_slopes``, ``doc_table``: ``mvp_attn_fwd_paged_scored``)."""
     lib = load_library()
     dev = q.device
     if k_cache.dim() == 4:
@@ -371,7 +435,11 @@ def attn_fwd_paged(q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_tab
             cu_seqlens_q.shape[0] - 1, total_q, int(max_q_len), int(max_k_len), int(num_decode_reqs), hq, hkv, d,
             _ptr(range_table), _ptr(range_covered), int(bool(causal)), int(window_left), int(window_right),
             _ptr(sinks), int(sink_mode), float(scale), _ptr(workspace), ws_bytes, _stream(stream, dev)]
-    if first_tokens != 0:
+    scores = _score_options(softcap, distance_slopes, doc_table, hq, total_q, dev)
+    if scores is not None:
+        args.insert(25, int(first_tokens))
+        name, st = "mvp_attn_fwd_paged_scored", _on(dev, lib.mvp_attn_fwd_paged_scored, (*args, scores))
+    elif first_tokens != 0:
         args.insert(25, int(first_tokens))
         name, st = "mvp_attn_fwd_paged_first", _on(dev, lib.mvp_attn_fwd_paged_first, args)
     else:

@@ -170,6 +170,21 @@ int mvp_fill_query_ranges(const int32_t* ranges, int num_reqs, int max_ranges, c
   return MVP_OK;
 }
 
+int mvp_fill_query_documents(const int32_t* doc_starts, int num_reqs, int max_docs, const int32_t* query_start_loc,
+                             const int32_t* seq_lens, int num_tokens, int32_t* out, int out_capacity, void* stream) {
+  g_last_launches = 0;
+  if (num_reqs < 0 || max_docs < 0 || num_tokens < 0 || out_capacity < 0) return MVP_ERR_ARG;
+  if (num_tokens == 0) return MVP_OK;
+  if (num_reqs < 1 || query_start_loc == nullptr || seq_lens == nullptr || out == nullptr) return MVP_ERR_ARG;
+  if (max_docs > 0 && doc_starts == nullptr) return MVP_ERR_ARG;
+  if (num_tokens > out_capacity) return MVP_ERR_CAPACITY;
+  if ((reinterpret_cast<uintptr_t>(out) & 7u) != 0) return MVP_ERR_UNSUPPORTED;
+  const DocFillParams p{doc_starts, query_start_loc, seq_lens, out, num_reqs, max_docs, num_tokens};
+  if (launch_fill_documents(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) return MVP_ERR_CUDA;
+  g_last_launches = 1;
+  return MVP_OK;
+}
+
 size_t mvp_attn_workspace_size(int num_reqs, int num_heads_q, int head_dim, int max_k_len) {
   if (num_reqs < 0 || num_heads_q <= 0 || head_dim <= 0 || max_k_len <= 0) return 0;
   int splits = (max_k_len + kDecodeChunk - 1) / kDecodeChunk;
@@ -248,7 +263,8 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
                   int causal, int window_left, int window_right, const float* sinks, int sink_mode, float scale,
                   void* workspace, size_t workspace_bytes, void* stream, const KVArgs& kv,
                   const int32_t* scan_ranges = nullptr, int max_ranges = 0,
-                  const mvp_attn_options* opts = nullptr, int first_tokens = 0) {
+                  const mvp_attn_options* opts = nullptr, int first_tokens = 0,
+                  const mvp_score_options* scores = nullptr) {
   const void* k = kv.k;
   const void* v = kv.v;
   const bool paged = kv.block_table != nullptr;
@@ -264,6 +280,9 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   if (window_left < 0) first_tokens = 0;  // every past key is visible already
   if (num_decode_reqs < -1 || num_decode_reqs > num_reqs) return MVP_ERR_ARG;
   if (!(scale > 0.f) || scale > 3.0e38f) return MVP_ERR_ARG;  // NaN, <= 0, inf
+  const float cap = scores != nullptr ? scores->softcap : 0.f;
+  if (!(cap >= 0.f) || cap > 1e30f || (cap > 0.f && cap < 1e-30f))
+    return MVP_ERR_ARG;  // (NaN among them; its reciprocal has to be a normal number)
   if (total_q == 0) return MVP_OK;
   if (kv.rows < 1 || kv.rows > INT_MAX || max_q_len < 1 || max_k_len < 1) return MVP_ERR_ARG;
   if (q == nullptr || k == nullptr || v == nullptr || out == nullptr || cu_seqlens_q == nullptr ||
@@ -277,6 +296,7 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   if (scan_ranges != nullptr && range_table != nullptr) return MVP_ERR_ARG;
   if (scan_ranges != nullptr && (reinterpret_cast<uintptr_t>(scan_ranges) & 7u) != 0) return MVP_ERR_UNSUPPORTED;
   if (static_cast<long long>(total_q) * num_heads_q * head_dim >= (1LL << 40)) return MVP_ERR_UNSUPPORTED;
+  if (scores != nullptr && (reinterpret_cast<uintptr_t>(scores->doc_table) & 7u) != 0) return MVP_ERR_UNSUPPORTED;
   if (opts != nullptr) {
     if (opts->variant != MVP_VARIANT_DEFAULT && opts->variant != MVP_VARIANT_D512_HEAD_SPLIT) return MVP_ERR_ARG;
     if (opts->variant == MVP_VARIANT_D512_HEAD_SPLIT && head_dim != 512) return MVP_ERR_UNSUPPORTED;
@@ -314,6 +334,10 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   m.scale = scale;
   m.wait_limit_us = (opts != nullptr && opts->wait_limit_us != 0) ? opts->wait_limit_us : kDefaultWaitLimitUs;
   m.fault = opts != nullptr ? opts->fault : kFaultNone;
+  m.sf.cap_log2 = cap * 1.4426950408889634f;
+  m.sf.inv_cap = cap > 0.f ? 1.f / m.sf.cap_log2 : 0.f;
+  m.sf.slopes = scores != nullptr ? scores->distance_slopes : nullptr;
+  m.sf.docs = scores != nullptr ? scores->doc_table : nullptr;
   m.total_q = total_q;
   m.err = err;
 
@@ -367,7 +391,7 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
     // batch with a 4096 window: 50 vs 52 % of peak); with ranges it measured
     // faster (mm-prefix sliding window: 62.4 vs 61.3 %, chunked prefill:
     // 90.6 vs 89.4 %).
-    const bool ranged = range_table != nullptr || scan_ranges != nullptr;
+    const bool ranged = range_table != nullptr || scan_ranges != nullptr || m.sf.docs != nullptr;
     pp.queue = (window_left < 0 || window_left >= max_k_len || ranged) ? queue : nullptr;
     if (!encode_3d(&pmq, q, head_dim, num_heads_q, total_q, 64, gpack, bmp, true) ||
         !encode_3d(&pmk, k, head_dim, num_heads_kv, total_k, 64, 1, box_rows(shape.k_box_keys), true) ||
@@ -527,6 +551,21 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
                              const int32_t* range_covered, int causal, int window_left, int window_right,
                              int first_tokens, const float* sinks, int sink_mode, float scale, void* workspace,
                              size_t workspace_bytes, void* stream) {
+  return mvp_attn_fwd_paged_scored(q, k_cache, v_cache, out, lse, cu_seqlens_q, seq_lens_k, block_table, block_size,
+                                   max_blocks_per_seq, num_blocks, context_lens, num_reqs, total_q, max_q_len,
+                                   max_k_len, num_decode_reqs, num_heads_q, num_heads_kv, head_dim, range_table,
+                                   range_covered, causal, window_left, window_right, first_tokens, sinks, sink_mode,
+                                   scale, workspace, workspace_bytes, stream, nullptr);
+}
+
+int mvp_attn_fwd_paged_scored(const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                             const int32_t* cu_seqlens_q, const int32_t* seq_lens_k, const int32_t* block_table,
+                             int block_size, int max_blocks_per_seq, int num_blocks, const int32_t* context_lens,
+                             int num_reqs, int total_q, int max_q_len, int max_k_len, int num_decode_reqs,
+                             int num_heads_q, int num_heads_kv, int head_dim, const int32_t* range_table,
+                             const int32_t* range_covered, int causal, int window_left, int window_right,
+                             int first_tokens, const float* sinks, int sink_mode, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream, const mvp_score_options* scores) {
   g_last_launches = 0;
   int shift = 0;
   while (shift < 30 && (1 << shift) < block_size) ++shift;
@@ -540,7 +579,7 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
   return attn_fwd_impl(q, out, lse, cu_seqlens_q, context_lens, num_reqs, total_q, max_q_len, max_k_len,
                        num_decode_reqs, num_heads_q, num_heads_kv, head_dim, range_table, range_covered, causal,
                        window_left, window_right, sinks, sink_mode, scale, workspace, workspace_bytes, stream, kv,
-                       nullptr, 0, nullptr, first_tokens);
+                       nullptr, 0, nullptr, first_tokens, scores);
 }
 
 int mvp_attn_fwd_varlen_first(const void* q, const void* k, const void* v, void* out, float* lse,
@@ -556,6 +595,21 @@ int mvp_attn_fwd_varlen_first(const void* q, const void* k, const void* v, void*
                        num_decode_reqs, num_heads_q, num_heads_kv, head_dim, range_table, range_covered, causal,
                        window_left, window_right, sinks, sink_mode, scale, workspace, workspace_bytes, stream, kv,
                        nullptr, 0, nullptr, first_tokens);
+}
+
+int mvp_attn_fwd_varlen_scored(const void* q, const void* k, const void* v, void* out, float* lse,
+                               const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, const int32_t* context_lens,
+                               int num_reqs, int total_q, int total_k, int max_q_len, int max_k_len,
+                               int num_decode_reqs, int num_heads_q, int num_heads_kv, int head_dim,
+                               const int32_t* range_table, const int32_t* range_covered, int causal, int window_left,
+                               int window_right, int first_tokens, const float* sinks, int sink_mode, float scale,
+                               void* workspace, size_t workspace_bytes, void* stream, const mvp_score_options* scores) {
+  g_last_launches = 0;
+  KVArgs kv{k, v, total_k, cu_seqlens_k, nullptr, nullptr, 0, 0};
+  return attn_fwd_impl(q, out, lse, cu_seqlens_q, context_lens, num_reqs, total_q, max_q_len, max_k_len,
+                       num_decode_reqs, num_heads_q, num_heads_kv, head_dim, range_table, range_covered, causal,
+                       window_left, window_right, sinks, sink_mode, scale, workspace, workspace_bytes, stream, kv,
+                       nullptr, 0, nullptr, first_tokens, scores);
 }
 
 int mvp_attn_fwd_varlen_scan(const void* q, const void* k, const void* v, void* out, float* lse,

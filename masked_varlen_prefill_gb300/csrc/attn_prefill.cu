@@ -22,6 +22,7 @@ PrefillShape prefill_tile_shape(int head_dim, bool d512_head_split) {
 
 cudaError_t launch_prefill(int head_dim, bool d512_head_split, const PrefillParams& p, const CUtensorMap& mq,
                            const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+  if (p.m.sf.any()) return launch_prefill_scored(head_dim, p, mq, mk, mv, stream);
   if (p.m.first_tokens > 0) return launch_prefill_first(head_dim, p, mq, mk, mv, stream);
   switch (head_dim) {
     case 64: return launch_cfg<Cfg64, false>(p, mq, mk, mv, stream);

@@ -1,6 +1,6 @@
 // Masked varlen attention forward, prefill rows: tcgen05 + TMA, sm_103a.
-// (Kernel and launch templates; attn_prefill.cu and attn_prefill_first.cu hold
-// the instantiations.)
+// (Kernel and launch templates; attn_prefill.cu, attn_prefill_first.cu and
+// attn_prefill_scored.cu hold the instantiations.)
 //
 // Computes, for 128-row query tiles, softmax(scale * Q K^T + mask) V with the
 // online (running max / running sum) formulation in base 2, as the Triton
@@ -399,7 +399,7 @@ __device__ __forceinline__ void queue_finish(unsigned long long* words, int n_cl
 // both CTAs of a pair walk the same tiles): the tiles between the smallest
 // and largest visible key of any row, and the tiles inside every row's
 // all-visible interval (no mask needed there).
-template <class C, bool FIRST>
+template <class C, bool FIRST, bool SCORED>
 __device__ __forceinline__ Plan plan_tiles(const Item& it, const PrefillParams& p, bool use_table, int lane) {
   int hl_min = INT_MAX, hh_max = INT_MIN, cl_max = INT_MIN, ch_min = INT_MAX;
   int fh_max = -1;  // last visible first token of any row
@@ -408,7 +408,12 @@ __device__ __forceinline__ Plan plan_tiles(const Item& it, const PrefillParams& 
     const int row = lane + 32 * k;
     const int qi = it.pos0 + row / p.gpack;
     if (qi < it.q_len) {
-      const RowVis v = row_visibility(p.m, it.ctx + qi, it.k_len, use_table, it.q0 + qi, it.b);
+      RowVis v = row_visibility(p.m, it.ctx + qi, it.k_len, use_table, it.q0 + qi, it.b);
+      int2 doc;
+      if constexpr (SCORED) {
+        doc = doc_entry(p.m, it.q0 + qi);
+        clip_to_doc(v, doc);
+      }
       int hl, hh, cl, ch;
       v.hull(hl, hh);
       v.core(cl, ch);
@@ -416,7 +421,11 @@ __device__ __forceinline__ Plan plan_tiles(const Item& it, const PrefillParams& 
         hl_min = min(hl_min, hl);
         hh_max = max(hh_max, hh);
       }
-      if constexpr (FIRST) fh_max = max(fh_max, first_tokens_hi(p.m, it.ctx + qi, it.k_len));
+      if constexpr (FIRST) {
+        int f_hi = first_tokens_hi(p.m, it.ctx + qi, it.k_len);
+        if constexpr (SCORED) f_hi = clip_first_to_doc(f_hi, doc);
+        fh_max = max(fh_max, f_hi);
+      }
       cl_max = max(cl_max, cl);  // an empty core (INT_MAX, INT_MIN) removes the interior
       ch_min = min(ch_min, ch);
     }
@@ -490,7 +499,9 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint
 // the log-sum-exp, so the softmax warps also sum the unrounded
 // probabilities; without it they skip that packed add per score pair (O
 // does not depend on it).  FIRST: the window leaves first tokens visible.
-template <class C, bool PAGED, bool LSE, bool FIRST>
+// SCORED: the scores go through a cap and a distance bias, and rows see only
+// their document's keys (each at run time).
+template <class C, bool PAGED, bool LSE, bool FIRST, bool SCORED>
 __global__ void __launch_bounds__(C::THREADS, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const PrefillParams p) {
@@ -1093,7 +1104,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ++qc;
         }
         if (!ok || item >= n_items) break;
-        e.pl = plan_tiles<C, FIRST>(e.it, p, use_table, lane);
+        e.pl = plan_tiles<C, FIRST, SCORED>(e.it, p, use_table, lane);
         e.last = 0;
         ok = publish(e);
       }
@@ -1127,7 +1138,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       RowVis vis;
       int f_hi;  // FIRST: last visible first token, or -1
       float sink;
+      int f_lo;     // SCORED: first visible first token
+      float slope;  // SCORED: distance bias per key, log2 units
     };
+    // SCORED: whether the scores are brought to log2 units before the maximum
+    // (a cap or a bias; documents alone leave them raw)
+    const bool scaled = SCORED && (p.m.sf.cap_log2 > 0.f || p.m.sf.slopes != nullptr);
     const int pos_off = row_pos_off();
     // p_full lives in rank 0: one arrival per warp (released at cluster scope in a pair)
     const uint32_t p_full_addr0 = C::PAIR ? mapa_shared(smem_u32(&sb.p_full[0]), 0) : 0u;
@@ -1141,6 +1157,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     struct RowLoads {
       int2 tab;
       float sink;
+      int2 doc;     // SCORED
+      float slope;  // SCORED
     };
     auto row_loads = [&](const PlanEntry& e) {
       RowLoads l;
@@ -1149,6 +1167,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       l.tab = (valid && use_table) ? range_entry(p.m, e.it.q0 + qi, e.it.b, e.it.ctx + qi) : make_int2(1, 0);
       l.sink = (!e.last && p.m.sink_mode != 0 && p.m.sinks != nullptr) ? __ldg(p.m.sinks + e.it.h0 + (row % p.gpack))
                                                                        : 0.f;
+      if constexpr (SCORED) {
+        l.doc = valid ? doc_entry(p.m, e.it.q0 + qi) : make_int2(0, INT_MAX);
+        l.slope = (!e.last && p.m.sf.slopes != nullptr)
+                      ? __ldg(p.m.sf.slopes + e.it.h0 + (row % p.gpack)) * 1.4426950408889634f
+                      : 0.f;
+      }
       return l;
     };
     auto row_ctx = [&](const PlanEntry& e, const RowLoads& l) {
@@ -1160,6 +1184,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       r.f_hi = -1;
       if constexpr (FIRST) {
         if (r.valid) r.f_hi = first_tokens_hi(p.m, e.it.ctx + r.qi, e.it.k_len);
+      }
+      if constexpr (SCORED) {
+        clip_to_doc(r.vis, l.doc);
+        r.f_hi = clip_first_to_doc(r.f_hi, l.doc);
+        r.f_lo = max(0, l.doc.x);
+        r.slope = l.slope;
       }
       r.sink = l.sink;
       return r;
@@ -1178,7 +1208,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const RowVis vis = rc.vis;
       const int f_hi = rc.f_hi;
       const float sink_l2 = rc.sink * 1.4426950408889634f;  // log2 units
-      const float sink_raw = rc.sink / p.m.scale;            // units of the raw q.k score
+      // (in the units of the scores when it is added: the raw q.k score's, or log2's)
+      const float sink_raw = SCORED && scaled ? sink_l2 : rc.sink / p.m.scale;
       float m_ref = null_mode ? sink_l2 : -INFINITY;
       // Partial row sums of this thread's columns: the bf16-rounded
       // probabilities (they normalise O, which the PV MMA builds from them;
@@ -1269,17 +1300,43 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ++xr;
         }
 
+        if constexpr (SCORED) {
+          // Capped and biased scores, in log2 units.
+          if (p.m.sf.cap_log2 > 0.f) {
+            const float c = p.m.sf.cap_log2, inv = p.m.sf.inv_cap;
+#pragma unroll
+            for (int i = 0; i < HC; ++i) s[i] = __float_as_uint(cap_score(__uint_as_float(s[i]) * sc, inv, c));
+          } else if (p.m.sf.slopes != nullptr) {
+            const uint64_t f = f2_pack(sc, sc);
+#pragma unroll
+            for (int i = 0; i < HC / 2; ++i) {
+              float a, b;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f), a, b);
+              s[2 * i] = __float_as_uint(a);
+              s[2 * i + 1] = __float_as_uint(b);
+            }
+          }
+          if (p.m.sf.slopes != nullptr) {
+            // distances are exact (below 2^24), so a bias is within half a unit
+            // in its last place
+            const float d0 = static_cast<float>(cur.it.ctx + rc.qi - (kb * BN + half * HC));
+#pragma unroll
+            for (int i = 0; i < HC; ++i)
+              s[i] = __float_as_uint(fmaf(-rc.slope, fabsf(d0 - static_cast<float>(i)), __uint_as_float(s[i])));
+          }
+        }
+
         // Mask: one bit per key of this thread's columns.  Scores stay in raw
         // q.k units; the scale folds into the exponent's FFMA (scale > 0).
         const bool masked = !(kb >= pl.int_lo && kb <= pl.int_hi) || (key0_mode && kb == 0);
         if (masked) {
           const int c0 = kb * BN + half * HC;  // first key of these columns
-          if (key0_mode && c0 == 0 && (vis.visible(0) || (FIRST && f_hi >= 0))) s[0] = __float_as_uint(__uint_as_float(s[0]) + sink_raw);
+          if (key0_mode && c0 == 0 && (vis.visible(0) || (FIRST && f_hi >= 0 && (!SCORED || rc.f_lo == 0)))) s[0] = __float_as_uint(__uint_as_float(s[0]) + sink_raw);
 #pragma unroll
           for (int w = 0; w < HC / 32; ++w) {
             uint32_t bits = interval_bits(vis.b_lo, vis.b_hi, c0 + 32 * w) |
                             interval_bits(vis.r_lo, vis.r_hi, c0 + 32 * w);
-            if constexpr (FIRST) bits |= interval_bits(0, f_hi, c0 + 32 * w);
+            if constexpr (FIRST) bits |= interval_bits(SCORED ? rc.f_lo : 0, f_hi, c0 + 32 * w);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               s[32 * w + i] = ((bits >> i) & 1u) ? s[32 * w + i] : __float_as_uint(-INFINITY);
@@ -1303,7 +1360,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           mx_raw = fmaxf(mx_raw, other.x);
         }
-        const float mx = mx_raw * sc;
+        const float sc_t = SCORED && scaled ? 1.f : sc;  // log2 units of a score as it now is
+        const float mx = mx_raw * sc_t;
         // lazy reference max
         float alpha = 1.f;
         const bool need = (mx > m_ref + kRescaleThreshold) || (m_ref == -INFINITY && mx > -INFINITY);
@@ -1314,7 +1372,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           m_ref = mx;
         }
         const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-        const uint64_t sc2 = f2_pack(sc, sc);
+        const uint64_t sc2 = f2_pack(sc_t, sc_t);
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
         uint64_t acc_e[4];
         float acc_lo[4], acc_hi[4];  // (MIXED_SUM: rounded probabilities of the even, odd columns)
@@ -1571,15 +1629,17 @@ struct LaunchState {
 };
 std::mutex g_launch_mutex;
 
-template <class C, bool FIRST>
+template <class C, bool FIRST, bool SCORED = false>
 cudaError_t launch_cfg(const PrefillParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                        cudaStream_t stream) {
   const bool paged = p.m.block_table != nullptr;
-  // (FIRST: one instantiation with and without an LSE buffer)
-  const bool want_lse = FIRST || p.lse != nullptr;
-  auto kern = paged ? (want_lse ? attn_prefill_kernel<C, true, true, FIRST> : attn_prefill_kernel<C, true, FIRST, FIRST>)
-                    : (want_lse ? attn_prefill_kernel<C, false, true, FIRST>
-                                : attn_prefill_kernel<C, false, FIRST, FIRST>);
+  // (FIRST, SCORED: one instantiation with and without an LSE buffer)
+  constexpr bool ONE = FIRST || SCORED;
+  const bool want_lse = ONE || p.lse != nullptr;
+  auto kern = paged ? (want_lse ? attn_prefill_kernel<C, true, true, FIRST, SCORED>
+                                : attn_prefill_kernel<C, true, ONE, FIRST, SCORED>)
+                    : (want_lse ? attn_prefill_kernel<C, false, true, FIRST, SCORED>
+                                : attn_prefill_kernel<C, false, ONE, FIRST, SCORED>);
   static LaunchState state[4][64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

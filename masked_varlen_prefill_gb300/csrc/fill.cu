@@ -39,11 +39,11 @@ constexpr int kMaxSpanRanges = 8 * kFillThreads;
 
 // Request b with qsl[b] <= t < qsl[b + 1] (requests with q_len 0 have
 // qsl[b] == qsl[b + 1] and never match).
-__device__ __forceinline__ int request_of(const FillParams& p, int t) {
-  int lo = 0, hi = p.num_reqs - 1;
+__device__ __forceinline__ int request_of(const int32_t* qsl, int num_reqs, int t) {
+  int lo = 0, hi = num_reqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.qsl + mid) <= t) lo = mid; else hi = mid - 1;
+    if (__ldg(qsl + mid) <= t) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_query_ranges_kernel(FillPar
         }
       } else {
         // Rows of many requests: scan the row's request in list order.
-        const int b = request_of(p, t);
+        const int b = request_of(p.qsl, p.num_reqs, t);
         const int first = __ldg(p.qsl + b);
         const int q_len = __ldg(p.qsl + b + 1) - first;
         const int q_abs = __ldg(p.seq_lens + b) - q_len + (t - first);
@@ -162,7 +162,37 @@ __global__ void __launch_bounds__(kFillThreads) fill_query_ranges_kernel(FillPar
   }
 }
 
+// Document table: a thread per row finds its request, then the first start
+// past its position, both by binary search (a row is 8 bytes written after
+// some log2(requests) + log2(documents) loads that its neighbours share:
+// latency-bound; 41 thousand rows of 3 requests take the time of the launch).
+__global__ void __launch_bounds__(kFillThreads) fill_query_documents_kernel(const DocFillParams p) {
+  griddep_launch_dependents();  // (as the range fill)
+  const int t = blockIdx.x * kFillThreads + threadIdx.x;
+  if (t >= p.num_tokens) return;
+  int2 e = make_int2(-1, -1);
+  if (t < __ldg(p.qsl + p.num_reqs)) {
+    const int b = request_of(p.qsl, p.num_reqs, t);
+    const int pos = __ldg(p.seq_lens + b) - (__ldg(p.qsl + b + 1) - t);
+    const int32_t* starts = p.doc_starts + static_cast<size_t>(b) * p.max_docs;
+    int lo = 0, hi = p.max_docs;  // the first start past pos lies in [lo, hi]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(starts + mid) <= pos) lo = mid + 1; else hi = mid;
+    }
+    e.x = lo > 0 ? __ldg(starts + lo - 1) : 0;
+    e.y = (lo < p.max_docs ? __ldg(starts + lo) : INT_MAX) - 1;
+  }
+  reinterpret_cast<int2*>(p.out)[t] = e;
+}
+
 }  // namespace
+
+cudaError_t launch_fill_documents(const DocFillParams& p, cudaStream_t stream) {
+  const int grid = (p.num_tokens - 1) / kFillThreads + 1;
+  fill_query_documents_kernel<<<grid, kFillThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_fill(const FillParams& p, cudaStream_t stream) {
   if (p.rows_written) {

@@ -139,6 +139,43 @@ __device__ __forceinline__ int first_tokens_hi(const MaskParams& m, int p, int k
   return hi < 0 ? -1 : static_cast<int>(hi);
 }
 
+// Documents that do not see each other: the closed key interval outside of
+// which packed query row `row` sees nothing (everything without documents).
+__device__ __forceinline__ int2 doc_entry(const MaskParams& m, int row) {
+  if (m.sf.docs == nullptr) return make_int2(0, INT_MAX);
+  if (!in_bounds(row, m.total_q, m.err)) return make_int2(0, -1);
+  return __ldg(reinterpret_cast<const int2*>(m.sf.docs) + row);
+}
+
+// The row's intervals cut to its document's (an empty one stays empty).
+__device__ __forceinline__ void clip_to_doc(RowVis& v, int2 doc) {
+  v.b_lo = max(v.b_lo, doc.x);
+  v.b_hi = min(v.b_hi, doc.y);
+  v.r_lo = max(v.r_lo, doc.x);
+  v.r_hi = min(v.r_hi, doc.y);
+}
+
+// First tokens under a document mask: those of the request that lie in the
+// row's document, [max(0, doc.x), the returned key], or -1 for none.
+__device__ __forceinline__ int clip_first_to_doc(int f_hi, int2 doc) {
+  f_hi = min(f_hi, doc.y);
+  return f_hi < max(0, doc.x) ? -1 : f_hi;
+}
+
+// x, a score in log2 units, capped: c tanh(x / c) with c = cap_log2 and
+// inv_cap = 1 / c.  Below |y| = |x / c| = 0.6: x P(y^2), P the minimax polynomial
+// of tanh(y) / y there (relative error 7e-8, 1.8e-7 evaluated in fp32).  Above:
+// c - 2 c / (1 + e^(2 y)), off by some 1.2e-7 c, and c or -c at the infinities.
+__device__ __forceinline__ float cap_score(float x, float inv_cap, float cap_log2) {
+  const float y = x * inv_cap, u = y * y;
+  float p = fmaf(u, 0.0154754277f, -0.0521014817f);
+  p = fmaf(u, p, 0.133101732f);
+  p = fmaf(u, p, -0.333323091f);
+  p = fmaf(u, p, 0.99999994f);
+  const float far = fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2_approx(y * 2.8853900817779268f)), cap_log2);
+  return fabsf(y) < 0.6f ? x * p : far;
+}
+
 // Row of a paged K/V cache (vLLM-style block table, block size
 // 2^block_shift) that holds key l of request b: the block id of l's block
 // times the block size plus l's offset in it.  Keys at or past the request's

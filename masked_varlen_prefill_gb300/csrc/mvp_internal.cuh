@@ -30,11 +30,35 @@ struct FillParams {
 
 cudaError_t launch_fill(const FillParams& p, cudaStream_t stream);
 
+struct DocFillParams {
+  const int32_t* doc_starts;  // [num_reqs, max_docs]
+  const int32_t* qsl;         // [num_reqs + 1]
+  const int32_t* seq_lens;    // [num_reqs]
+  int32_t* out;               // [num_tokens, 2]
+  int num_reqs;
+  int max_docs;
+  int num_tokens;             // > 0
+};
+
+cudaError_t launch_fill_documents(const DocFillParams& p, cudaStream_t stream);
+
 // Faults a caller can ask for to test the bounded-wait path (never set by
 // the plain entry points).  kFaultWithholdProbs: the first softmax warp of
 // every prefill CTA (rank 0 of each pair) does not signal that its first key
 // tile's probabilities are in TMEM, so the MMA issuer's wait for them runs out.
 enum FaultInjection : int { kFaultNone = 0, kFaultWithholdProbs = 1 };
+
+// ----------------------------------------------------------------- scores
+// Functions of the score, and documents that do not see each other.  In log2
+// units a score x = scale log2(e) q.k becomes c tanh(x / c) with a cap c, and
+// slope[h] log2(e) |p - j| is subtracted.
+struct ScoreParams {
+  float cap_log2;         // the cap, times log2(e); 0: none
+  float inv_cap;          // 1 / cap_log2
+  const float* slopes;    // [hq] or null: no distance bias
+  const int32_t* docs;    // [total_q, 2] or null: closed key interval of the row's document
+  __host__ __device__ bool any() const { return cap_log2 > 0.f || slopes != nullptr || docs != nullptr; }
+};
 
 // ----------------------------------------------------------------- masks
 // Per-row visible set = base interval U range interval (closed, in key
@@ -61,6 +85,7 @@ struct MaskParams {
   float scale;               // > 0
   uint32_t wait_limit_us;    // budget of one bounded device wait
   int fault;                 // FaultInjection: kFaultNone except in the timeout tests
+  ScoreParams sf;            // functions of the score (kernels instantiated for them)
   // bounds-checked build: rows of q / out / table, and the error word
   int total_q;
   int* err;
@@ -116,6 +141,10 @@ cudaError_t launch_prefill(int head_dim, bool d512_head_split, const PrefillPara
 cudaError_t launch_prefill_first(int head_dim, const PrefillParams& p, const CUtensorMap& map_q,
                                  const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
 
+// launch_prefill's kernels for m.sf.any() (the default variants, with or without first tokens).
+cudaError_t launch_prefill_scored(int head_dim, const PrefillParams& p, const CUtensorMap& map_q,
+                                  const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
+
 // ----------------------------------------------------------------- decode
 struct DecodeParams {
   MaskParams m;
@@ -135,6 +164,11 @@ struct DecodeParams {
 
 cudaError_t launch_decode(int head_dim, const DecodeParams& p, const CUtensorMap& map_k,
                           const CUtensorMap& map_v, cudaStream_t stream, int* launches);
+// launch_decode's kernels for m.sf.any(), without and with first tokens.
+cudaError_t launch_decode_scored(int head_dim, const DecodeParams& p, const CUtensorMap& map_k,
+                                 const CUtensorMap& map_v, cudaStream_t stream, int* launches);
+cudaError_t launch_decode_scored_first(int head_dim, const DecodeParams& p, const CUtensorMap& map_k,
+                                       const CUtensorMap& map_v, cudaStream_t stream, int* launches);
 int decode_keys_per_tile(int head_dim);
 int decode_box_inner(int head_dim);
 // Heads one decode CTA handles for a GQA group of `group` query heads.
