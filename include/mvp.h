@@ -2,9 +2,10 @@
  * mvp.h -- masked varlen prefill attention for GB300 (sm_103a), C ABI.
  *
  * Two operations, as described by the vLLM pages this library restates (and,
- * next to them, the steps of a bounded paged cache: rotary positions written
- * into it, first tokens that stay visible, the weight each key received, and
- * eviction by it):
+ * next to them, functions of the score, the steps of a bounded paged cache:
+ * rotary positions written into it, first tokens that stay visible, the weight
+ * each key received, eviction by it; and the pages of a pool, taken, shared,
+ * freed and compacted):
  *
  *   mvp_fill_query_ranges  -- vLLM PR #50294 review ("FA4 mm_prefix range
  *       scan -> O(1) table lookup"), "Implementation breakdown" step 1 and the
@@ -777,6 +778,99 @@ int mvp_kv_evict_paged(void* k_cache, void* v_cache, const float* weights, float
 /* Bytes of workspace mvp_kv_evict_paged needs (0 for non-positive sizes). */
 size_t mvp_kv_evict_workspace_size(int num_reqs, int num_heads_kv, int budget);
 
+/*
+ * The pages of a pool of paged K/V caches: taken, shared, freed and compacted
+ * on the device.  A pool is num_blocks pages of block_size tokens in each of
+ * num_caches caches (K and V of every layer that goes by the same block
+ * tables), and
+ *   refs  int32 [num_blocks], how many table entries hold each page; a page is
+ *         free when that is <= 0.  Zeroed by the caller for an empty pool.
+ * Request b holds the first ceil(seq_lens_k[b] / block_size) entries of its
+ * row of block_table, the pages that the attention calls read for it (they,
+ * mvp_rope_append_paged and mvp_kv_evict_paged use the tables as they are).
+ * Whoever else holds pages (a prefix cache) adds to their refs.  Results are
+ * the same in every run.  All are integers or bits: there is nothing to round.
+ *
+ * caches        HOST array of num_caches (0..256) device pointers, 16-byte
+ *               aligned, each [num_blocks, block_size] rows of row_bytes bytes
+ *               (num_heads_kv * head_dim * the element size; a multiple of 16),
+ *               no two overlapping.  Read before the call returns.
+ * block_table   int32 [num_reqs, max_blocks_per_seq].  Ids outside
+ *               [0, num_blocks) are left out of every step.
+ * block_size    16, 32, 64, 128 or 256.
+ * Calls on one pool are ordered by the caller (one stream, or events).
+ * Errors of all: MVP_ERR_ARG, MVP_ERR_UNSUPPORTED (alignment, row_bytes, more
+ * than 256 caches), MVP_ERR_CAPACITY (workspace), MVP_ERR_CUDA.
+ */
+
+/*
+ * Room for add_lens[b] (int32 [num_reqs], >= 0) more tokens in each request:
+ * new_seq_lens[b] = seq_lens_k[b] + add_lens[b] (new_seq_lens may be
+ * seq_lens_k).  Pages are taken lowest id first, for the requests in order and
+ * within one in the order of its tokens; their refs become 1.  A request that
+ * appends to a partly filled page that has other holders (refs > 1 at the
+ * start of the call) takes a page in its place first: the filled rows are
+ * copied in every cache, and the old page loses a holder (when all its holders
+ * append in one call, it is free afterwards).  The new tokens' rows are not
+ * written.  At most 65535 requests.
+ * missing       int32 device scalar: 0, or the number of pages that the pool
+ *               lacks, or -1 when a length is negative or a new length exceeds
+ *               max_blocks_per_seq * block_size.  Unless it is 0 nothing is
+ *               changed, and new_seq_lens is seq_lens_k.
+ * workspace     device scratch of mvp_kv_extend_workspace_size bytes, 16-byte
+ *               aligned, no initialisation needed.  Two calls that may run at
+ *               the same time need separate workspaces.
+ */
+int mvp_kv_extend_paged(void* const* caches, int num_caches, size_t row_bytes, int32_t* refs, int num_blocks,
+                        int32_t* block_table, int max_blocks_per_seq, int block_size, const int32_t* seq_lens_k,
+                        const int32_t* add_lens, int32_t* new_seq_lens, int num_reqs, int32_t* missing,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mvp_kv_extend_paged needs (0 for num_reqs <= 0). */
+size_t mvp_kv_extend_workspace_size(int num_reqs);
+
+/*
+ * A new batch whose rows continue rows of the old one (samples of a prompt, a
+ * beam step, a batch without its finished requests): row i of block_table_out
+ * (int32 [num_out, max_blocks_out], max_blocks_out >= max_blocks_per_seq) and
+ * seq_lens_out[i] become row parents[i]'s; a parent outside [0, num_reqs)
+ * gives a request without tokens.  Pages are shared, not copied: the pages of
+ * a row with c continuations gain c - 1 holders, so those of a row that
+ * nothing continues lose one.  Entries past a request's pages are not written.
+ * The new arrays do not overlap the old ones, whose rows no longer hold pages
+ * afterwards.
+ */
+int mvp_kv_fork_paged(int32_t* refs, int num_blocks, const int32_t* block_table, const int32_t* seq_lens_k,
+                      int num_reqs, int max_blocks_per_seq, const int32_t* parents, int num_out,
+                      int32_t* block_table_out, int max_blocks_out, int32_t* seq_lens_out, int block_size,
+                      void* stream);
+
+/*
+ * Cuts each request with 0 <= new_seq_lens[b] < seq_lens_k[b] to that length
+ * (in seq_lens_k): its pages past it lose a holder.  0 frees the request; other
+ * values leave it as it is.  The table's entries are not written.
+ */
+int mvp_kv_trim_paged(int32_t* refs, int num_blocks, const int32_t* block_table, int max_blocks_per_seq,
+                      int32_t* seq_lens_k, const int32_t* new_seq_lens, int num_reqs, int block_size, void* stream);
+
+/*
+ * Moves the live pages (refs > 0) to the lowest ids: of n live pages, those
+ * with ids >= n move, in ascending order, to the free ids below n, in ascending
+ * order, in every cache and with their refs; the rest stay.
+ * block_table   the requests' entries (num_reqs may be 0) name the new ids.
+ * block_map     int32 [num_blocks], written: the new id of each live page, -1
+ *               for a free one (for holders outside the tables).
+ * num_live      int32 device scalar, written: n.
+ * workspace     device scratch of mvp_kv_compact_workspace_size bytes, as above.
+ */
+int mvp_kv_compact_paged(void* const* caches, int num_caches, size_t row_bytes, int32_t* refs, int num_blocks,
+                         int32_t* block_table, int max_blocks_per_seq, int block_size, const int32_t* seq_lens_k,
+                         int num_reqs, int32_t* block_map, int32_t* num_live, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mvp_kv_compact_paged needs (0 for num_blocks <= 0). */
+size_t mvp_kv_compact_workspace_size(int num_blocks);
+
 /* Synchronises `stream`, returns MVP_ERR_DEVICE_TIMEOUT if a kernel recorded a
  * timeout since the last call (and clears it), MVP_ERR_DEVICE_BOUNDS if a
  * kernel of the bounds-checked build (libmvp_debug.so, compiled with
@@ -789,8 +883,7 @@ int mvp_get_last_device_error(void* stream);
 const char* mvp_status_str(int status);
 
 /* Number of kernel launches the last successful mvp_attn_* /
- * mvp_fill_query_ranges / mvp_rope_append_paged / mvp_kv_evict_paged call
- * enqueued on this thread (for launch accounting). */
+ * mvp_fill_query_* / mvp_rope_append_paged / mvp_kv_* call enqueued on this thread (for launch accounting). */
 int mvp_last_launch_count(void);
 
 #ifdef __cplusplus

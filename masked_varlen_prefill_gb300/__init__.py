@@ -43,6 +43,16 @@ from ._lib import (  # noqa: F401
     meta_block_layout,
     meta_pack,
 )
+from ._pages import (  # noqa: F401
+    KVCaches,
+    kv_caches,
+    kv_compact_paged,
+    kv_compact_workspace_size,
+    kv_extend_paged,
+    kv_extend_workspace_size,
+    kv_fork_paged,
+    kv_trim_paged,
+)
 from ._cache import (  # noqa: F401
     RopeTable,
     attn_key_weights_paged,

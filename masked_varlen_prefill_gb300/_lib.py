@@ -114,6 +114,12 @@ _SIGNATURES = {
     "mvp_kv_evict_workspace_size": (_sz, [_i, _i, _i]),
     "mvp_kv_evict_paged": (_i, [_vp, _vp, _vp, _vp, _i, _ll, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i,
                                 _i, _vp, _vp, _vp, _sz, _vp]),
+    "mvp_kv_extend_workspace_size": (_sz, [_i]),
+    "mvp_kv_compact_workspace_size": (_sz, [_i]),
+    "mvp_kv_extend_paged": (_i, [_vp, _i, _sz, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "mvp_kv_fork_paged": (_i, [_vp, _i, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _vp]),
+    "mvp_kv_trim_paged": (_i, [_vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp]),
+    "mvp_kv_compact_paged": (_i, [_vp, _i, _sz, _vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
     "mvp_attn_accounting": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(AttnCounts)]),
 }
 
