@@ -351,7 +351,8 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
  * the document does, and first_tokens are the request's, seen by rows of the
  * document that holds them.
  *
- * softcap         0 (no cap) or 1e-30 .. 1e30.
+ * softcap         0 (no cap) or 1e-30 .. 1e30, and softcap / scale within
+ *                 1e-37 .. 1e37 (MVP_ERR_UNSUPPORTED otherwise).
  * distance_slopes fp32 [num_heads_q], any finite values, or NULL.  Distances
  *                 up to 2^24 are exact.
  * doc_table       int32 [total_q, 2], 8-byte aligned, or NULL: the closed key

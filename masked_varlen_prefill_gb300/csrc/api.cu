@@ -336,6 +336,19 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   m.fault = opts != nullptr ? opts->fault : kFaultNone;
   m.sf.cap_log2 = cap * 1.4426950408889634f;
   m.sf.inv_cap = cap > 0.f ? 1.f / m.sf.cap_log2 : 0.f;
+  const double rate = cap > 0.f ? static_cast<double>(scale) / cap : 0.0;
+  m.sf.inv_cap_raw = static_cast<float>(rate);
+  m.sf.cap_raw = cap > 0.f ? static_cast<float>(1.0 / rate) : 0.f;
+  if (cap > 0.f && !(rate > 1e-37 && rate < 1e37)) return MVP_ERR_UNSUPPORTED;
+  const double u = rate * rate;
+  const float tanh2[] = {kTanh2_1, kTanh2_2}, tanh3[] = {kTanh3_1, kTanh3_2, kTanh3_3},
+              tanh4[] = {kTanh1, kTanh2, kTanh3, kTanh4};
+  for (int i = 0; i < 2; ++i) m.sf.near2[i] = static_cast<float>(tanh2[i] * std::pow(u, i + 1));
+  for (int i = 0; i < 3; ++i) m.sf.near3[i] = static_cast<float>(tanh3[i] * std::pow(u, i + 1));
+  for (int i = 0; i < 4; ++i) m.sf.near4[i] = static_cast<float>(tanh4[i] * std::pow(u, i + 1));
+  const float near[] = {kTanhNear2, kTanhNear3, kTanhNear};
+  // (coefficients past fp32's range: every score takes the other way)
+  for (int i = 0; i < 3; ++i) m.sf.cap_near[i] = std::isfinite(m.sf.near4[3]) ? near[i] * m.sf.cap_raw : 0.f;
   m.sf.slopes = scores != nullptr ? scores->distance_slopes : nullptr;
   m.sf.docs = scores != nullptr ? scores->doc_table : nullptr;
   m.total_q = total_q;

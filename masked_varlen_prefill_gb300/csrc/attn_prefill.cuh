@@ -73,6 +73,8 @@ namespace {
 constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr unsigned kFullMask = 0xffffffffu;
+// Bits of the kernel's SCORE argument.
+constexpr int kScored = 1, kCapped = 2, kBiased = 4;
 
 template <int D_, int DV_, int BN_, int KST_, int VST_, int NCTA_, int SPLITD_ = 0, int NS_ = 2, int ROWSUM_ = 0>
 struct Cfg {
@@ -223,10 +225,15 @@ struct Plan {
   int kb_lo, n_tiles, int_lo, int_hi, n_first, first_k16;
 };
 
-// Key tile of the item's step j.
-template <bool FIRST>
+// Key tile of the item's step j.  BACK: from the last tile to the first.  Under
+// a distance bias the nearest keys weigh most: walked towards them, the running
+// maximum rises in every tile of a head whose bias grows by more than the
+// rescale threshold over a tile, and each rise rescales O (2 x 8192 rows, 32/8
+// heads, D = 128, slopes 2^-0.25 .. 2^-8: 1245 us, BACKTIME backwards).
+template <bool FIRST, bool BACK>
 __device__ __forceinline__ int tile_of(const Plan& pl, int j) {
   if constexpr (FIRST) return j < pl.n_first ? j : pl.kb_lo + j - pl.n_first;
+  else if constexpr (BACK) return pl.kb_lo + pl.n_tiles - 1 - j;
   else return pl.kb_lo + j;
 }
 // Tiles from kb_lo on.
@@ -499,12 +506,15 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint
 // the log-sum-exp, so the softmax warps also sum the unrounded
 // probabilities; without it they skip that packed add per score pair (O
 // does not depend on it).  FIRST: the window leaves first tokens visible.
-// SCORED: the scores go through a cap and a distance bias, and rows see only
-// their document's keys (each at run time).
-template <class C, bool PAGED, bool LSE, bool FIRST, bool SCORED>
+// SCORE: functions of the score (kScored bits): rows see only their document's
+// keys, and scores may go through a cap and a distance bias (each at run time;
+// an instantiation without a bit has none of its code: with all of it, documents
+// alone cost 15 % of the time on whole prompts at D = 128).
+template <class C, bool PAGED, bool LSE, bool FIRST, int SCORE>
 __global__ void __launch_bounds__(C::THREADS, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const PrefillParams p) {
+  constexpr bool SCORED = SCORE != 0, CAP = (SCORE & kCapped) != 0, BIAS = (SCORE & kBiased) != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Barriers sb;
@@ -684,7 +694,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       };
       int cbuf = 0;  // ids buffer of the current item
       auto prefetch_kv = [&](const PlanEntry& e, int j) {  // packed K / V only
-        const int key0 = e.it.k0 + tile_of<FIRST>(e.pl, j) * BN;
+        const int key0 = e.it.k0 + tile_of<FIRST, BIAS>(e.pl, j) * BN;
 #pragma unroll
         for (int c = 0; c < C::QCH; ++c)
           tma_prefetch_l2_3d(&map_k, dq0 + c * 64, e.it.hkv, key0 + (C::PAIR ? rank * C::KROWS : 0));
@@ -744,7 +754,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (!free) return false;
         }
         if (leader) mbar_arrive_expect_tx(&sb.k_full[s], C::MMA_CTAS * C::K_BYTES);
-        const int key0 = tile_of<FIRST>(e.pl, j) * BN + (C::PAIR ? rank * C::KROWS : 0);  // this CTA's first key of the tile
+        const int key0 = tile_of<FIRST, BIAS>(e.pl, j) * BN + (C::PAIR ? rank * C::KROWS : 0);  // this CTA's first key of the tile
         if constexpr (PAGED) {
           // one box per run of K rows inside one cache block (a rolled loop:
           // the producer's code stays small next to the other roles')
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (!free) return false;
         }
         if (leader) mbar_arrive_expect_tx(&sb.v_full[s], C::MMA_CTAS * C::V_BYTES);
-        const int key0 = tile_of<FIRST>(e.pl, j) * BN;
+        const int key0 = tile_of<FIRST, BIAS>(e.pl, j) * BN;
         if constexpr (PAGED) {
 #pragma unroll 1
           for (int r = 0; r < BN; r += vbox) {
@@ -1139,11 +1149,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int f_hi;  // FIRST: last visible first token, or -1
       float sink;
       int f_lo;     // SCORED: first visible first token
-      float slope;  // SCORED: distance bias per key, log2 units
+      float slope;  // SCORED: distance bias per key, q.k units
     };
-    // SCORED: whether the scores are brought to log2 units before the maximum
-    // (a cap or a bias; documents alone leave them raw)
-    const bool scaled = SCORED && (p.m.sf.cap_log2 > 0.f || p.m.sf.slopes != nullptr);
     const int pos_off = row_pos_off();
     // p_full lives in rank 0: one arrival per warp (released at cluster scope in a pair)
     const uint32_t p_full_addr0 = C::PAIR ? mapa_shared(smem_u32(&sb.p_full[0]), 0) : 0u;
@@ -1167,10 +1174,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       l.tab = (valid && use_table) ? range_entry(p.m, e.it.q0 + qi, e.it.b, e.it.ctx + qi) : make_int2(1, 0);
       l.sink = (!e.last && p.m.sink_mode != 0 && p.m.sinks != nullptr) ? __ldg(p.m.sinks + e.it.h0 + (row % p.gpack))
                                                                        : 0.f;
-      if constexpr (SCORED) {
-        l.doc = valid ? doc_entry(p.m, e.it.q0 + qi) : make_int2(0, INT_MAX);
+      if constexpr (SCORED) l.doc = valid ? doc_entry(p.m, e.it.q0 + qi) : make_int2(0, INT_MAX);
+      if constexpr (BIAS) {
         l.slope = (!e.last && p.m.sf.slopes != nullptr)
-                      ? __ldg(p.m.sf.slopes + e.it.h0 + (row % p.gpack)) * 1.4426950408889634f
+                      ? __ldg(p.m.sf.slopes + e.it.h0 + (row % p.gpack)) / p.m.scale
                       : 0.f;
       }
       return l;
@@ -1189,8 +1196,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         clip_to_doc(r.vis, l.doc);
         r.f_hi = clip_first_to_doc(r.f_hi, l.doc);
         r.f_lo = max(0, l.doc.x);
-        r.slope = l.slope;
       }
+      if constexpr (BIAS) r.slope = l.slope;
       r.sink = l.sink;
       return r;
     };
@@ -1207,9 +1214,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const Plan& pl = cur.pl;
       const RowVis vis = rc.vis;
       const int f_hi = rc.f_hi;
+      // SCORED: no row of this warp sees a key ahead of it
+      const bool behind = BIAS && __all_sync(kFullMask, max(vis.b_hi, vis.r_hi) <= cur.it.ctx + rc.qi);
       const float sink_l2 = rc.sink * 1.4426950408889634f;  // log2 units
-      // (in the units of the scores when it is added: the raw q.k score's, or log2's)
-      const float sink_raw = SCORED && scaled ? sink_l2 : rc.sink / p.m.scale;
+      const float sink_raw = rc.sink / p.m.scale;            // units of the raw q.k score
       float m_ref = null_mode ? sink_l2 : -INFINITY;
       // Partial row sums of this thread's columns: the bf16-rounded
       // probabilities (they normalise O, which the PV MMA builds from them;
@@ -1258,7 +1266,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         const int j = C::SPLITD ? js - 1 : js;
         const int t = T + j;
-        const int kb = tile_of<FIRST>(pl, j);
+        const int kb = tile_of<FIRST, BIAS>(pl, j);
         const uint32_t scol = tmem + lane_base + C::S_COL + C::sbuf(t) * BN;
         if (!C::SPLITD && !mbar_wait(&sb.s_full[C::sbuf(t)], C::sphase(t), &sb.wc, p.err, kDevTimeoutMma)) {
           ok = false;
@@ -1300,57 +1308,128 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ++xr;
         }
 
-        if constexpr (SCORED) {
-          // Capped and biased scores, in log2 units.
+        // Mask: one bit per key of this thread's columns.  Scores stay in raw
+        // q.k units; the scale folds into the exponent's FFMA (scale > 0).
+        const bool masked = !(kb >= pl.int_lo && kb <= pl.int_hi) || (key0_mode && kb == 0);
+        auto mask_bits = [&](int w) {
+          const int c = kb * BN + half * HC + 32 * w;
+          uint32_t bits = interval_bits(vis.b_lo, vis.b_hi, c) | interval_bits(vis.r_lo, vis.r_hi, c);
+          if constexpr (FIRST) bits |= interval_bits(SCORED ? rc.f_lo : 0, f_hi, c);
+          return bits;
+        };
+        // Capped and biased scores, still in q.k units.
+        if constexpr (CAP) {
           if (p.m.sf.cap_log2 > 0.f) {
-            const float c = p.m.sf.cap_log2, inv = p.m.sf.inv_cap;
+            if (masked) {  // masked scores, which may be anything, do not decide how the others are capped
 #pragma unroll
-            for (int i = 0; i < HC; ++i) s[i] = __float_as_uint(cap_score(__uint_as_float(s[i]) * sc, inv, c));
-          } else if (p.m.sf.slopes != nullptr) {
-            const uint64_t f = f2_pack(sc, sc);
+              for (int w = 0; w < HC / 32; ++w) {
+                const uint32_t bits = mask_bits(w);
 #pragma unroll
-            for (int i = 0; i < HC / 2; ++i) {
-              float a, b;
-              f2_unpack(f2_mul(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f), a, b);
-              s[2 * i] = __float_as_uint(a);
-              s[2 * i + 1] = __float_as_uint(b);
+                for (int i = 0; i < 32; ++i) s[32 * w + i] = ((bits >> i) & 1u) ? s[32 * w + i] : 0u;
+              }
+            }
+            float far8[8];  // the largest |s|
+#pragma unroll
+            for (int k = 0; k < 8; ++k) far8[k] = fmaxf(fabsf(__uint_as_float(s[k])), fabsf(__uint_as_float(s[k + 8])));
+#pragma unroll
+            for (int i = 16; i < HC; i += 16)
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                far8[k] = fmax3(far8[k], fabsf(__uint_as_float(s[i + k])), fabsf(__uint_as_float(s[i + 8 + k])));
+            const float far = fmax3(fmax3(far8[0], far8[1], far8[2]), fmax3(far8[3], far8[4], far8[5]),
+                                    fmaxf(far8[6], far8[7]));
+            // Where all scores of this warp's part of the tile are well below the
+            // cap (the usual case), a polynomial alone, two scores at a time, of
+            // the degree that the largest of them asks for.
+            const float cap_r = p.m.sf.cap_raw;
+            auto near = [&](float limit) { return __all_sync(kFullMask, far < limit || !rc.valid); };
+            auto poly = [&](auto... c) {
+              const float co[] = {c...};
+              constexpr int N = sizeof...(c);
+#pragma unroll
+              for (int i = 0; i < HC / 2; ++i) {
+                const uint64_t x = f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                const uint64_t u = f2_mul(x, x);
+                uint64_t q = f2_pack(co[N - 1], co[N - 1]);
+#pragma unroll
+                for (int k = N - 2; k >= 0; --k) q = f2_fma(u, q, f2_pack(co[k], co[k]));
+                float x0, x1;
+                f2_unpack(f2_mul(x, q), x0, x1);
+                s[2 * i] = __float_as_uint(x0);
+                s[2 * i + 1] = __float_as_uint(x1);
+              }
+            };
+            const ScoreParams& f = p.m.sf;
+            if (near(f.cap_near[0])) poly(kTanh2_0, f.near2[0], f.near2[1]);
+            else if (near(f.cap_near[1])) poly(kTanh3_0, f.near3[0], f.near3[1], f.near3[2]);
+            else if (near(f.cap_near[2])) poly(kTanh0, f.near4[0], f.near4[1], f.near4[2], f.near4[3]);
+            else {
+#pragma unroll
+              for (int i = 0; i < HC; ++i) s[i] = __float_as_uint(cap_score(__uint_as_float(s[i]), f.inv_cap_raw, cap_r));
             }
           }
-          if (p.m.sf.slopes != nullptr) {
-            // distances are exact (below 2^24), so a bias is within half a unit
-            // in its last place
-            const float d0 = static_cast<float>(cur.it.ctx + rc.qi - (kb * BN + half * HC));
+        }
+        // Distance bias.  Behind the row it is -slope (d0 - i) at column i, d0 the
+        // first column's distance: slope (i % 8) is added to the scores here, and
+        // group_bias, the same for eight columns, to their maximum and in the
+        // exponent (one packed add per pair of scores).
+        float d0 = 0.f, lin = 0.f;
+        auto group_bias = [&](int g) { return -lin * (d0 - 8.f * g); };
+        if constexpr (BIAS) {
+          // Distances are exact (below 2^24), so a bias is within half a unit in
+          // its last place.  Rows of this warp that see no key ahead of them
+          // take distances as they are (a masked key's may be negative).
+          d0 = static_cast<float>(cur.it.ctx + rc.qi - (kb * BN + half * HC));
+          if (behind || __all_sync(kFullMask, d0 >= static_cast<float>(HC - 1))) {
+            lin = rc.slope;
+#pragma unroll
+            for (int i = 0; i < HC / 2; ++i) {
+              const int c = (2 * i) % 8;
+              float x0, x1;
+              f2_unpack(f2_add(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                               f2_pack(lin * c, lin * (c + 1))),
+                        x0, x1);
+              s[2 * i] = __float_as_uint(x0);
+              s[2 * i + 1] = __float_as_uint(x1);
+            }
+          } else {
 #pragma unroll
             for (int i = 0; i < HC; ++i)
               s[i] = __float_as_uint(fmaf(-rc.slope, fabsf(d0 - static_cast<float>(i)), __uint_as_float(s[i])));
           }
         }
 
-        // Mask: one bit per key of this thread's columns.  Scores stay in raw
-        // q.k units; the scale folds into the exponent's FFMA (scale > 0).
-        const bool masked = !(kb >= pl.int_lo && kb <= pl.int_hi) || (key0_mode && kb == 0);
         if (masked) {
           const int c0 = kb * BN + half * HC;  // first key of these columns
           if (key0_mode && c0 == 0 && (vis.visible(0) || (FIRST && f_hi >= 0 && (!SCORED || rc.f_lo == 0)))) s[0] = __float_as_uint(__uint_as_float(s[0]) + sink_raw);
 #pragma unroll
           for (int w = 0; w < HC / 32; ++w) {
-            uint32_t bits = interval_bits(vis.b_lo, vis.b_hi, c0 + 32 * w) |
-                            interval_bits(vis.r_lo, vis.r_hi, c0 + 32 * w);
-            if constexpr (FIRST) bits |= interval_bits(SCORED ? rc.f_lo : 0, f_hi, c0 + 32 * w);
+            const uint32_t bits = mask_bits(w);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               s[32 * w + i] = ((bits >> i) & 1u) ? s[32 * w + i] : __float_as_uint(-INFINITY);
           }
         }
-        float mx8[8];
+        float mx_raw;
+        if constexpr (BIAS) {
+          float mg[HC / 8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 8]));
+          for (int g = 0; g < HC / 8; ++g) {
+            auto x = [&](int i) { return __uint_as_float(s[8 * g + i]); };
+            mg[g] = fmax3(fmax3(x(0), x(1), x(2)), fmax3(x(3), x(4), x(5)), fmaxf(x(6), x(7))) + group_bias(g);
+          }
+          mx_raw = fmax3(fmax3(mg[0], mg[1], mg[2]), fmax3(mg[3], mg[4], mg[5]), fmaxf(mg[6], mg[7]));
+        } else {
+          float mx8[8];
 #pragma unroll
-        for (int i = 16; i < HC; i += 16)
+          for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 8]));
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mx8[k] = fmax3(mx8[k], __uint_as_float(s[i + k]), __uint_as_float(s[i + 8 + k]));
-        float mx_raw = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+          for (int i = 16; i < HC; i += 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mx8[k] = fmax3(mx8[k], __uint_as_float(s[i + k]), __uint_as_float(s[i + 8 + k]));
+          mx_raw = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+        }
         if constexpr (C::SPLIT > 1) {
           // the two halves of a row meet once per tile
           float2 other;
@@ -1360,8 +1439,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           mx_raw = fmaxf(mx_raw, other.x);
         }
-        const float sc_t = SCORED && scaled ? 1.f : sc;  // log2 units of a score as it now is
-        const float mx = mx_raw * sc_t;
+        const float mx = mx_raw * sc;
         // lazy reference max
         float alpha = 1.f;
         const bool need = (mx > m_ref + kRescaleThreshold) || (m_ref == -INFINITY && mx > -INFINITY);
@@ -1372,8 +1450,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           m_ref = mx;
         }
         const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-        const uint64_t sc2 = f2_pack(sc_t, sc_t);
-        const uint64_t nm2 = f2_pack(-m_use, -m_use);
+        const uint64_t sc2 = f2_pack(sc, sc);
+        uint64_t nm2 = f2_pack(-m_use, -m_use);
         uint64_t acc_e[4];
         float acc_lo[4], acc_hi[4];  // (MIXED_SUM: rounded probabilities of the even, odd columns)
 #pragma unroll
@@ -1383,6 +1461,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
 #pragma unroll
         for (int i = 0; i < HC / 2; ++i) {
+          if constexpr (BIAS) {
+            if (i % 4 == 0) {
+              const float nm = fmaf(group_bias(i / 4), sc, -m_use);
+              nm2 = f2_pack(nm, nm);
+            }
+          }
           float t0, t1;
           f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2), t0, t1);
           const float e0 = ex2_approx(t0);
@@ -1629,17 +1713,17 @@ struct LaunchState {
 };
 std::mutex g_launch_mutex;
 
-template <class C, bool FIRST, bool SCORED = false>
+template <class C, bool FIRST, int SCORE = 0>
 cudaError_t launch_cfg(const PrefillParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                        cudaStream_t stream) {
   const bool paged = p.m.block_table != nullptr;
-  // (FIRST, SCORED: one instantiation with and without an LSE buffer)
-  constexpr bool ONE = FIRST || SCORED;
+  // (FIRST, SCORE: one instantiation with and without an LSE buffer)
+  constexpr bool ONE = FIRST || SCORE != 0;
   const bool want_lse = ONE || p.lse != nullptr;
-  auto kern = paged ? (want_lse ? attn_prefill_kernel<C, true, true, FIRST, SCORED>
-                                : attn_prefill_kernel<C, true, ONE, FIRST, SCORED>)
-                    : (want_lse ? attn_prefill_kernel<C, false, true, FIRST, SCORED>
-                                : attn_prefill_kernel<C, false, ONE, FIRST, SCORED>);
+  auto kern = paged ? (want_lse ? attn_prefill_kernel<C, true, true, FIRST, SCORE>
+                                : attn_prefill_kernel<C, true, ONE, FIRST, SCORE>)
+                    : (want_lse ? attn_prefill_kernel<C, false, true, FIRST, SCORE>
+                                : attn_prefill_kernel<C, false, ONE, FIRST, SCORE>);
   static LaunchState state[4][64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -1,0 +1,20 @@
+// Prefill attention with a distance bias: instantiations of
+// attn_prefill.cuh.  Translation units of their own, like
+// attn_prefill_first.cu, so that the others stay what they are and all
+// compile in parallel.
+#include "attn_prefill.cuh"
+
+namespace mvp {
+
+cudaError_t launch_prefill_biased(int head_dim, const PrefillParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                                  const CUtensorMap& mv, cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_cfg<Cfg64, false, kScored | kBiased>(p, mq, mk, mv, stream);
+    case 128: return launch_cfg<Cfg128, false, kScored | kBiased>(p, mq, mk, mv, stream);
+    case 256: return launch_cfg<Cfg256, false, kScored | kBiased>(p, mq, mk, mv, stream);
+    case 512: return launch_cfg<Cfg512, false, kScored | kBiased>(p, mq, mk, mv, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace mvp

@@ -162,18 +162,17 @@ __device__ __forceinline__ int clip_first_to_doc(int f_hi, int2 doc) {
   return f_hi < max(0, doc.x) ? -1 : f_hi;
 }
 
-// x, a score in log2 units, capped: c tanh(x / c) with c = cap_log2 and
-// inv_cap = 1 / c.  Below |y| = |x / c| = 0.6: x P(y^2), P the minimax polynomial
-// of tanh(y) / y there (relative error 7e-8, 1.8e-7 evaluated in fp32).  Above:
-// c - 2 c / (1 + e^(2 y)), off by some 1.2e-7 c, and c or -c at the infinities.
-__device__ __forceinline__ float cap_score(float x, float inv_cap, float cap_log2) {
-  const float y = x * inv_cap, u = y * y;
-  float p = fmaf(u, 0.0154754277f, -0.0521014817f);
-  p = fmaf(u, p, 0.133101732f);
-  p = fmaf(u, p, -0.333323091f);
-  p = fmaf(u, p, 0.99999994f);
-  const float far = fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2_approx(y * 2.8853900817779268f)), cap_log2);
-  return fabsf(y) < 0.6f ? x * p : far;
+// x capped: c tanh(x / c), inv = 1 / c.  Below |y| = |x / c| = kTanhNear: x times
+// the polynomial of tanh(y) / y.  Above: c - 2 c / (1 + e^(2 y)), off by some
+// 1.2e-7 c, and c or -c at the infinities.
+__device__ __forceinline__ float cap_score(float x, float inv, float c) {
+  const float y = x * inv, u = y * y;
+  float p = fmaf(u, kTanh4, kTanh3);
+  p = fmaf(u, p, kTanh2);
+  p = fmaf(u, p, kTanh1);
+  p = fmaf(u, p, kTanh0);
+  const float far = fmaf(-2.f * c, rcp_approx(1.f + ex2_approx(y * 2.8853900817779268f)), c);
+  return fabsf(y) < kTanhNear ? x * p : far;
 }
 
 // Row of a paged K/V cache (vLLM-style block table, block size

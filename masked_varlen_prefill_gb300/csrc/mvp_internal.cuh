@@ -52,9 +52,24 @@ enum FaultInjection : int { kFaultNone = 0, kFaultWithholdProbs = 1 };
 // Functions of the score, and documents that do not see each other.  In log2
 // units a score x = scale log2(e) q.k becomes c tanh(x / c) with a cap c, and
 // slope[h] log2(e) |p - j| is subtracted.
+// tanh(y) / y for |y| <= T as a polynomial in y^2, minimax in the relative
+// error: of degree 2 for T = 0.25 (4.0e-7), 3 for 0.4 (9.8e-8), 4 for 0.6 (7.3e-8;
+// fp32 arithmetic adds some 1e-7).
+constexpr float kTanhNear2 = 0.25f, kTanhNear3 = 0.4f, kTanhNear = 0.6f;
+constexpr float kTanh2_0 = 0.999999583f, kTanh2_1 = -0.333219081f, kTanh2_2 = 0.128416136f;
+constexpr float kTanh3_0 = 0.999999881f, kTanh3_1 = -0.333313614f, kTanh3_2 = 0.132709771f, kTanh3_3 = -0.0475536026f;
+constexpr float kTanh0 = 0.99999994f, kTanh1 = -0.333323091f, kTanh2 = 0.133101732f, kTanh3 = -0.0521014817f,
+                kTanh4 = 0.0154754277f;
+
 struct ScoreParams {
   float cap_log2;         // the cap, times log2(e); 0: none
   float inv_cap;          // 1 / cap_log2
+  // The prefill kernels' scores stay in units of q.k: the cap is cap_raw = softcap
+  // / scale, and the polynomials above take u = s^2 (their first coefficient
+  // needs no scaling); cap_near: the |s| below which each holds.
+  float cap_raw, inv_cap_raw;
+  float cap_near[3];
+  float near2[2], near3[3], near4[4];
   const float* slopes;    // [hq] or null: no distance bias
   const int32_t* docs;    // [total_q, 2] or null: closed key interval of the row's document
   __host__ __device__ bool any() const { return cap_log2 > 0.f || slopes != nullptr || docs != nullptr; }
@@ -141,9 +156,18 @@ cudaError_t launch_prefill(int head_dim, bool d512_head_split, const PrefillPara
 cudaError_t launch_prefill_first(int head_dim, const PrefillParams& p, const CUtensorMap& map_q,
                                  const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
 
-// launch_prefill's kernels for m.sf.any() (the default variants, with or without first tokens).
-cudaError_t launch_prefill_scored(int head_dim, const PrefillParams& p, const CUtensorMap& map_q,
-                                  const CUtensorMap& map_k, const CUtensorMap& map_v, cudaStream_t stream);
+// launch_prefill's kernels for m.sf.any() (the default variants), and those it
+// chooses from.
+#define MVP_LAUNCH_PREFILL(name)                                                                                \
+  cudaError_t name(int head_dim, const PrefillParams& p, const CUtensorMap& map_q, const CUtensorMap& map_k, \
+                   const CUtensorMap& map_v, cudaStream_t stream)
+MVP_LAUNCH_PREFILL(launch_prefill_scored);
+MVP_LAUNCH_PREFILL(launch_prefill_docs);
+MVP_LAUNCH_PREFILL(launch_prefill_capped);
+MVP_LAUNCH_PREFILL(launch_prefill_biased);
+MVP_LAUNCH_PREFILL(launch_prefill_capped_biased);
+MVP_LAUNCH_PREFILL(launch_prefill_scored_first);
+#undef MVP_LAUNCH_PREFILL
 
 // ----------------------------------------------------------------- decode
 struct DecodeParams {
