@@ -6,6 +6,7 @@ namespace mvp {
 
 int decode_keys_per_tile(int head_dim) { return kt_for(head_dim); }
 int decode_box_inner(int head_dim) { return box_for(head_dim); }
+int decode_ctas_per_sm(int head_dim) { return head_dim == 512 ? 1 : head_dim == 128 ? 3 : 2; }
 
 cudaError_t launch_decode(int head_dim, const DecodeParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
                           cudaStream_t stream, int* launches) {

@@ -133,7 +133,7 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
   constexpr int PPL = pairs_for(D, GP);  // probabilities per lane and step
   constexpr int KG = 32 * PPL / GP;      // keys per warp step
   constexpr int NG = C::KT / KG;     // warp steps per tile
-  static_assert(C::NW * GP * (D + 2) * 4 <= C::STAGES * 2 * C::TILE, "merge buffers fit the stages");
+  static_assert((C::NW + 1) * GP * (D + 2) * 4 <= C::STAGES * 2 * C::TILE, "merge buffers fit the stages");
   static_assert(C::KT % KG == 0, "whole steps per tile");
   extern __shared__ uint8_t smem_raw[];
   // Per compute warp, the step's 32 probabilities (key kk, head g at
@@ -145,7 +145,11 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int sp = blockIdx.x;
+  // SCORED: the CTAs of a cluster share a split's keys, and join their results
+  // through distributed shared memory.
+  const int part = blockIdx.x;
+  const int ctas = SCORED ? static_cast<int>(cluster_ctas()) : 1;
+  const int sp = SCORED ? part / ctas : part;
   const int b = blockIdx.y;
   const int n_sub = (p.group + GP - 1) / GP;
   const int hkv = blockIdx.z / n_sub;
@@ -193,12 +197,19 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
   const int n_first = FIRST && f_hi >= 0 ? min((f_hi + C::KT) & ~(C::KT - 1), lo) : 0;
   const int skip = lo - n_first;  // keys between the first tokens' tiles and the hull's
   const int n_walk = (lo <= hi || n_first > 0) ? n_first + (hi - lo + 1) : 0;
-  const int w_lo = sp * p.chunk;
+  // SCORED: the row's parts are alike, of at least min_chunk keys (a document
+  // may be much shorter than the longest request, which chunk is made for).
+  int chunk = p.chunk;
+  if constexpr (SCORED) {
+    const int parts = static_cast<int>(gridDim.x);
+    chunk = max(((n_walk + parts - 1) / parts + C::KT - 1) / C::KT * C::KT, p.min_chunk);
+  }
+  const int w_lo = static_cast<int>(min(static_cast<long long>(part) * chunk, static_cast<long long>(n_walk)));
   // (without first tokens n_first = 0: the walk is the hull's)
-  const int n_keys = max(0, min(n_walk - w_lo, p.chunk));
+  const int n_keys = max(0, min(n_walk - w_lo, chunk));
   const int n_tiles = (n_keys + C::KT - 1) / C::KT;
   const bool single = p.partial == nullptr;
-  if (n_keys == 0 && !single) {
+  if (n_keys == 0 && !single && ctas == 1) {
     // An empty split still publishes a neutral partial for the combine.
     float* part = p.partial + ((static_cast<size_t>(b) * p.hq + hq0) * p.n_splits + sp) * (D + 2);
     for (int g = 0; g < heads_here; ++g) {
@@ -207,7 +218,7 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
     }
     return;
   }
-  if (n_keys == 0 && sp > 0) return;
+  if (n_keys == 0 && sp > 0 && ctas == 1) return;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -411,20 +422,38 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
           }
         }
         x[a] = v[0];
-        if constexpr (SCORED) {
-          if (p.m.sf.cap_log2 > 0.f) x[a] = cap_score(x[a], p.m.sf.inv_cap, p.m.sf.cap_log2);
-          if (p.m.sf.slopes != nullptr) x[a] = fmaf(-my_slope, fabsf(static_cast<float>(pos - (t0 + kk))), x[a]);
-        }
-        if (!interior) {
+        if (!SCORED && !interior) {
           const int key = t0 + kk;
           if (key0_mode && key == 0) x[a] += my_sink;
-          if (!vis.visible(key) && !(FIRST && key <= f_hi && (!SCORED || key >= doc.x))) x[a] = -INFINITY;
+          if (!vis.visible(key) && !(FIRST && key <= f_hi)) x[a] = -INFINITY;
+        }
+      }
+      if constexpr (SCORED) {
+        // Only this lane's own pairs (sub-steps rr + r * DUP) go through the
+        // functions and the mask; they move to x[0 .. PPL).
+#pragma unroll
+        for (int r = 0; r < PPL; ++r) {
+          float xr = x[r * DUP];
+#pragma unroll
+          for (int a = 1; a < DUP; ++a) xr = (rr == a) ? x[r * DUP + a] : xr;
+          const int key = t0 + gi * KG + (r * DUP + rr) * KS + ks;
+          if (p.m.sf.cap_log2 > 0.f) xr = cap_score(xr, p.m.sf.inv_cap, p.m.sf.cap_log2);
+          if (p.m.sf.slopes != nullptr) xr = fmaf(-my_slope, fabsf(static_cast<float>(pos - key)), xr);
+          if (!interior) {
+            if (key0_mode && key == 0) xr += my_sink;
+            if (!vis.visible(key) && !(FIRST && key <= f_hi && key >= doc.x)) xr = -INFINITY;
+          }
+          x[r] = xr;
         }
       }
       // max of head hh over the step's keys: this lane's NSUB, then the KS keys
       float mx = x[0];
 #pragma unroll
-      for (int a = 1; a < NSUB; ++a) mx = fmaxf(mx, x[a]);
+      for (int a = 1; a < (SCORED ? PPL : NSUB); ++a) mx = fmaxf(mx, x[a]);
+      if constexpr (SCORED) {
+#pragma unroll
+        for (int o = 1; o < DUP; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      }
 #pragma unroll
       for (int o = DS; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
       const bool need = mx > m_h + kRescaleThreshold;
@@ -442,9 +471,11 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
       }
 #pragma unroll
       for (int r = 0; r < PPL; ++r) {  // this lane's pairs: sub-steps rr + r * DUP
-        float xr = x[r * DUP];
+        float xr = x[SCORED ? r : r * DUP];
+        if constexpr (!SCORED) {
 #pragma unroll
-        for (int a = 1; a < DUP; ++a) xr = (rr == a) ? x[r * DUP + a] : xr;
+          for (int a = 1; a < DUP; ++a) xr = (rr == a) ? x[r * DUP + a] : xr;
+        }
         const float pr = (xr == -INFINITY) ? 0.f : ex2_approx(xr - m_h);
         l_part += pr;
         pb[((r * DUP + rr) * KS + ks) * GP + hh] = f2_pack(pr, pr);
@@ -497,18 +528,52 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
   asm volatile("bar.sync 1, %0;" ::"r"(C::NW * 32) : "memory");
 
   const bool null_mode = p.m.sink_mode == 2 && p.m.sinks != nullptr;
-  for (int idx = threadIdx.x; idx < heads_here * D; idx += C::NW * 32) {
+  float* joined = sml + C::NW * GP * 2;  // SCORED, cluster: this CTA's result, [GP][D], then [GP][max, sum]
+  if (SCORED && ctas > 1) {
+    for (int idx = threadIdx.x; idx < heads_here * D; idx += C::NW * 32) {
+      const int g = idx / D, d = idx % D;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) M = fmaxf(M, sml[(w * GP + g) * 2]);
+      float a = 0.f, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) {
+        const float mw = sml[(w * GP + g) * 2];
+        const float f = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
+        a += f * sm[(w * GP + g) * D + d];
+        L += f * sml[(w * GP + g) * 2 + 1];
+      }
+      joined[idx] = a;
+      if (d == 0) {
+        joined[GP * D + 2 * g] = M;
+        joined[GP * D + 2 * g + 1] = L;
+      }
+    }
+    cluster_sync_all();
+  }
+  const int first_idx = SCORED && ctas > 1 ? part % ctas * (C::NW * 32) : 0;
+  for (int idx = first_idx + threadIdx.x; idx < heads_here * D; idx += ctas * (C::NW * 32)) {
     const int g = idx / D, d = idx % D;
-    float M = -INFINITY;
+    float M = -INFINITY, a = 0.f, L = 0.f;
+    if (SCORED && ctas > 1) {
+      const uint32_t ml = smem_u32(joined + GP * D + 2 * g), ad = smem_u32(joined + idx);
+      for (int r = 0; r < ctas; ++r) M = fmaxf(M, ld_cluster_f32(mapa_shared(ml, r)));
+      for (int r = 0; r < ctas; ++r) {
+        const float mr = ld_cluster_f32(mapa_shared(ml, r));
+        const float f = (mr == -INFINITY) ? 0.f : ex2_approx(mr - M);
+        a += f * ld_cluster_f32(mapa_shared(ad, r));
+        L += f * ld_cluster_f32(mapa_shared(ml, r) + 4);
+      }
+    } else {
 #pragma unroll
-    for (int w = 0; w < C::NW; ++w) M = fmaxf(M, sml[(w * GP + g) * 2]);
-    float a = 0.f, L = 0.f;
+      for (int w = 0; w < C::NW; ++w) M = fmaxf(M, sml[(w * GP + g) * 2]);
 #pragma unroll
-    for (int w = 0; w < C::NW; ++w) {
-      const float mw = sml[(w * GP + g) * 2];
-      const float f = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
-      a += f * sm[(w * GP + g) * D + d];
-      L += f * sml[(w * GP + g) * 2 + 1];
+      for (int w = 0; w < C::NW; ++w) {
+        const float mw = sml[(w * GP + g) * 2];
+        const float f = (mw == -INFINITY) ? 0.f : ex2_approx(mw - M);
+        a += f * sm[(w * GP + g) * D + d];
+        L += f * sml[(w * GP + g) * 2 + 1];
+      }
     }
     const int h = hq0 + g;
     if (!single) {
@@ -538,6 +603,7 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
     }
   }
   (void)ok;
+  if (SCORED && ctas > 1) cluster_sync_all();  // (the peers have read this CTA's result)
 }
 
 template <int D, int GP, bool PAGED, bool FIRST>
@@ -547,8 +613,10 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
   decode_rows<D, GP, PAGED, FIRST, false>(map_k, map_v, p);
 }
 
+// Registers for as many CTAs per SM as shared memory holds (a warp scheduler
+// has room for three warps of up to 168 registers, and a CTA has five warps).
 template <int D, int GP, bool PAGED, bool FIRST>
-__global__ void __launch_bounds__(DCfg<D>::THREADS)
+__global__ void __launch_bounds__(DCfg<D>::THREADS, D == 512 ? 1 : D == 128 && GP <= 4 ? 3 : 2)
     attn_decode_scored_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                               const __grid_constant__ DecodeParams p) {
   decode_rows<D, GP, PAGED, FIRST, true>(map_k, map_v, p);
@@ -623,7 +691,22 @@ cudaError_t launch_dg(const DecodeParams& p, const CUtensorMap& mk, const CUtens
     }
   }
   const int n_sub = (p.group + GP - 1) / GP;
-  dim3 grid(p.n_splits, p.num_reqs, p.hkv * n_sub);
+  dim3 grid(p.n_splits * p.cluster, p.num_reqs, p.hkv * n_sub);
+  if (SCORED && p.cluster > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = p.cluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(DCfg<D>::THREADS);
+    cfg.dynamicSmemBytes = DCfg<D>::SMEM;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
+  }
   kern<<<grid, DCfg<D>::THREADS, DCfg<D>::SMEM, stream>>>(mk, mv, p);
   return cudaGetLastError();
 }

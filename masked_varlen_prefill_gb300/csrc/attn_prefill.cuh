@@ -1340,7 +1340,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                     fmaxf(far8[6], far8[7]));
             // Where all scores of this warp's part of the tile are well below the
             // cap (the usual case), a polynomial alone, two scores at a time, of
-            // the degree that the largest of them asks for.
+            // the degree that the largest of them asks for.  (Left to the
+            // exponent's FFMA, with the polynomial as its factor, it would be an
+            // instruction less per pair, but it measured 2-6 % slower.)
             const float cap_r = p.m.sf.cap_raw;
             auto near = [&](float limit) { return __all_sync(kFullMask, far < limit || !rc.valid); };
             auto poly = [&](auto... c) {
@@ -1365,16 +1367,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             else if (near(f.cap_near[2])) poly(kTanh0, f.near4[0], f.near4[1], f.near4[2], f.near4[3]);
             else {
 #pragma unroll
-              for (int i = 0; i < HC; ++i) s[i] = __float_as_uint(cap_score(__uint_as_float(s[i]), f.inv_cap_raw, cap_r));
+              for (int i = 0; i < HC / 2; ++i) {
+                float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
+                cap_scores(x0, x1, f.inv_cap_raw, cap_r);
+                s[2 * i] = __float_as_uint(x0);
+                s[2 * i + 1] = __float_as_uint(x1);
+              }
             }
           }
         }
         // Distance bias.  Behind the row it is -slope (d0 - i) at column i, d0 the
         // first column's distance: slope (i % 8) is added to the scores here, and
-        // group_bias, the same for eight columns, to their maximum and in the
+        // -lin (d0 - 8 g), the same for eight columns, to their maximum and in the
         // exponent (one packed add per pair of scores).
         float d0 = 0.f, lin = 0.f;
-        auto group_bias = [&](int g) { return -lin * (d0 - 8.f * g); };
         if constexpr (BIAS) {
           // Distances are exact (below 2^24), so a bias is within half a unit in
           // its last place.  Rows of this warp that see no key ahead of them
@@ -1412,13 +1418,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         float mx_raw;
         if constexpr (BIAS) {
+          // the columns' maxima, group g's 8 g lin above the first group's
           float mg[HC / 8];
 #pragma unroll
           for (int g = 0; g < HC / 8; ++g) {
             auto x = [&](int i) { return __uint_as_float(s[8 * g + i]); };
-            mg[g] = fmax3(fmax3(x(0), x(1), x(2)), fmax3(x(3), x(4), x(5)), fmaxf(x(6), x(7))) + group_bias(g);
+            mg[g] = fmax3(fmax3(x(0), x(1), x(2)), fmax3(x(3), x(4), x(5)), fmaxf(x(6), x(7)));
           }
-          mx_raw = fmax3(fmax3(mg[0], mg[1], mg[2]), fmax3(mg[3], mg[4], mg[5]), fmaxf(mg[6], mg[7]));
+#pragma unroll
+          for (int n = 1; n < HC / 8; n *= 2)
+#pragma unroll
+            for (int g = 0; g < HC / 8; g += 2 * n) mg[g] = fmaxf(mg[g], fmaf(8.f * n, lin, mg[g + n]));
+          mx_raw = fmaf(-lin, d0, mg[0]);
         } else {
           float mx8[8];
 #pragma unroll
@@ -1459,16 +1470,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           acc_e[k] = 0ull;
           acc_lo[k] = acc_hi[k] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < HC / 2; ++i) {
-          if constexpr (BIAS) {
-            if (i % 4 == 0) {
-              const float nm = fmaf(group_bias(i / 4), sc, -m_use);
-              nm2 = f2_pack(nm, nm);
-            }
-          }
+        auto prob_pair = [&](int i, uint64_t t) {
           float t0, t1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2), t0, t1);
+          f2_unpack(t, t0, t1);
           const float e0 = ex2_approx(t0);
           const float e1 = ex2_approx(t1);
           const uint32_t pk = pack_bf16x2(e0, e1);
@@ -1476,6 +1480,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             add_bf16x2_halves(pk, acc_lo[i & 3], acc_hi[i & 3]);
           if constexpr (LSE) acc_e[i & 3] = f2_add(acc_e[i & 3], f2_pack(e0, e1));
           s[i] = pk;
+        };
+        auto score_pair = [&](int i) { return f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])); };
+        if constexpr (BIAS) {
+          const float nm = fmaf(-lin * d0, sc, -m_use), step = 8.f * lin * sc;
+          nm2 = f2_pack(nm, nm);
+          const uint64_t step2 = f2_pack(step, step);
+#pragma unroll
+          for (int i = 0; i < HC / 2; ++i) {
+            if (i > 0 && i % 4 == 0) nm2 = f2_add(nm2, step2);
+            prob_pair(i, f2_fma(score_pair(i), sc2, nm2));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < HC / 2; ++i) prob_pair(i, f2_fma(score_pair(i), sc2, nm2));
         }
         {
           float a0, a1, b0, b1;

@@ -175,6 +175,24 @@ __device__ __forceinline__ float cap_score(float x, float inv, float c) {
   return fabsf(y) < kTanhNear ? x * p : far;
 }
 
+// Two of them: the products and sums by packed instructions.
+__device__ __forceinline__ void cap_scores(float& x0, float& x1, float inv, float c) {
+  const auto both = [](float v) { return f2_pack(v, v); };
+  const uint64_t x = f2_pack(x0, x1), y = f2_mul(x, both(inv)), u = f2_mul(y, y);
+  uint64_t q = f2_fma(u, both(kTanh4), both(kTanh3));
+  q = f2_fma(u, q, both(kTanh2));
+  q = f2_fma(u, q, both(kTanh1));
+  q = f2_fma(u, q, both(kTanh0));
+  float near0, near1, e0, e1, far0, far1, y0, y1;
+  f2_unpack(f2_mul(x, q), near0, near1);
+  f2_unpack(f2_mul(y, both(2.8853900817779268f)), e0, e1);
+  f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), both(1.f)), e0, e1);
+  f2_unpack(f2_fma(both(-2.f * c), f2_pack(rcp_approx(e0), rcp_approx(e1)), both(c)), far0, far1);
+  f2_unpack(y, y0, y1);
+  x0 = fabsf(y0) < kTanhNear ? near0 : far0;
+  x1 = fabsf(y1) < kTanhNear ? near1 : far1;
+}
+
 // Row of a paged K/V cache (vLLM-style block table, block size
 // 2^block_shift) that holds key l of request b: the block id of l's block
 // times the block size plus l's offset in it.  Keys at or past the request's

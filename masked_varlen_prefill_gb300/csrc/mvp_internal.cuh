@@ -183,7 +183,9 @@ struct DecodeParams {
   int hkv;
   int group;            // hq / hkv
   int n_splits;
-  int chunk;            // keys per split
+  int chunk;            // keys per split (plain kernels)
+  int cluster;          // CTAs that share a split (1 but for functions of the score)
+  int min_chunk;        // functions of the score: keys of a CTA's part, at least
 };
 
 cudaError_t launch_decode(int head_dim, const DecodeParams& p, const CUtensorMap& map_k,
@@ -195,6 +197,7 @@ cudaError_t launch_decode_scored_first(int head_dim, const DecodeParams& p, cons
                                        const CUtensorMap& map_v, cudaStream_t stream, int* launches);
 int decode_keys_per_tile(int head_dim);
 int decode_box_inner(int head_dim);
+int decode_ctas_per_sm(int head_dim);  // that shared memory holds
 // Heads one decode CTA handles for a GQA group of `group` query heads.
 inline int decode_heads_per_cta(int head_dim, int group) {
   if (group == 1) return 1;

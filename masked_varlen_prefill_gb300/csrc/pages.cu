@@ -50,12 +50,6 @@ struct Caches {
   long long page_bytes;  // block_size rows
 };
 
-__device__ __forceinline__ uint32_t cluster_ctas() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-
 // Exclusive prefix sum over the CTA's threads, and the sum.
 template <class T>
 __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
