@@ -26,7 +26,9 @@ class KVCaches:
         self.num_blocks = num_blocks
         self.row_bytes = row_bytes
         self.device = tensors[0].device
-        self.pointers = (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+        self.count = len(tensors)
+        self._array = (ctypes.c_void_p * self.count)(*[t.data_ptr() for t in tensors])
+        self.pointers = ctypes.addressof(self._array)
 
 
 def kv_caches(caches, block_size) -> KVCaches:
@@ -49,31 +51,36 @@ def kv_caches(caches, block_size) -> KVCaches:
     return KVCaches(tensors, block_size, rows // block_size, shape[-1] * shape[-2] * tensors[0].element_size())
 
 
-def _pool(refs, num_blocks=None):
-    dev = _cuda_device(refs, "refs")
-    _need(dev, _I32, "refs", refs)
-    if refs.dim() != 1 or (num_blocks is not None and refs.shape[0] != num_blocks):
-        raise ValueError("refs must be [num_blocks]")
-    return dev
+# These calls run every step on small arrays, where their host time is what a
+# caller waits for: one pass over the tensors, and messages only when it fails.
+def _checked(refs, num_blocks, *named):
+    """refs [num_blocks] and name, tensor, shape, name, tensor, shape, ...: all
+    int32, contiguous and on refs' device, which is returned.  A shape of None:
+    a table of two dimensions."""
+    dev = refs.device
+    if refs.is_cuda and refs.dtype is _I32 and refs.is_contiguous() and refs.shape == (num_blocks,):
+        for t, shape in zip(named[1::3], named[2::3]):
+            if not (t.dtype is _I32 and t.device == dev and t.is_contiguous() and
+                    (t.shape == shape if shape is not None else t.dim() == 2)):
+                break
+        else:
+            return dev
+    _need(_cuda_device(refs, "refs"), _I32, "refs", refs)
+    if refs.shape != (num_blocks,):
+        raise ValueError(f"refs must be [{num_blocks}]")
+    for name, t, shape in zip(named[::3], named[1::3], named[2::3]):
+        _need(dev, _I32, name, t)
+        if shape is None and t.dim() != 2:
+            raise ValueError(f"{name} must be [B, max_blocks]")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError("arguments of a pool must be int32 tensors on one device")
 
 
-def _rows(dev, block_table, name, **lens):
-    """Table [B, max_blocks] and lengths [B], all int32 on dev; B."""
-    _need(dev, _I32, name, block_table)
-    if block_table.dim() != 2:
-        raise ValueError(f"{name} must be [B, max_blocks]")
-    for n, t in lens.items():
-        _need(dev, _I32, n, t)
-        if t.shape != block_table.shape[:1]:
-            raise ValueError(f"{n} must be [B]")
-    return block_table.shape[0]
-
-
-def _scalar_and_workspace(dev, name, scalar, workspace):
-    _need(dev, _I32, name, scalar)
-    if scalar.numel() != 1:
-        raise ValueError(f"{name} must be one int32")
-    _need(dev, torch.uint8, "workspace", workspace)
+def _workspace(workspace, dev):
+    if not (workspace.dtype is torch.uint8 and workspace.device == dev and workspace.is_contiguous()):
+        _need(dev, torch.uint8, "workspace", workspace)
+    return workspace.data_ptr(), workspace.numel()
 
 
 def kv_extend_workspace_size(num_reqs) -> int:
@@ -95,14 +102,14 @@ def kv_extend_paged(caches, refs, block_table, seq_lens_k, add_lens, new_seq_len
     bytes.  All or nothing: ``missing`` is 0, or says how many pages the pool
     lacks (-1: a length that the table cannot hold) and nothing has changed.
     """
-    dev = _pool(refs, caches.num_blocks)
+    b = block_table.shape[:1]
+    dev = _checked(refs, caches.num_blocks, "block_table", block_table, None, "seq_lens_k", seq_lens_k, b, "add_lens",
+                   add_lens, b, "new_seq_lens", new_seq_lens, b, "missing", missing, (1,))
     if caches.device != dev:
         raise ValueError(f"the caches must be on {dev}")
-    n = _rows(dev, block_table, "block_table", seq_lens_k=seq_lens_k, add_lens=add_lens, new_seq_lens=new_seq_lens)
-    _scalar_and_workspace(dev, "missing", missing, workspace)
-    _call("mvp_kv_extend_paged", dev, stream, caches.pointers, len(caches.tensors), caches.row_bytes, refs.data_ptr(),
+    _call("mvp_kv_extend_paged", dev, stream, caches.pointers, caches.count, caches.row_bytes, refs.data_ptr(),
           caches.num_blocks, block_table.data_ptr(), block_table.shape[1], caches.block_size, seq_lens_k.data_ptr(),
-          add_lens.data_ptr(), new_seq_lens.data_ptr(), n, missing.data_ptr(), workspace.data_ptr(), workspace.numel())
+          add_lens.data_ptr(), new_seq_lens.data_ptr(), b[0], missing.data_ptr(), *_workspace(workspace, dev))
 
 
 def kv_fork_paged(refs, block_table, seq_lens_k, parents, block_table_out, seq_lens_out, block_size, *, stream=None):
@@ -111,11 +118,11 @@ def kv_fork_paged(refs, block_table, seq_lens_k, parents, block_table_out, seq_l
     ``mvp_kv_fork_paged`` in include/mvp.h).  parents int32 [B_out]; the new
     table int32 [B_out, >= max_blocks] and lengths int32 [B_out] are written,
     in memory of their own."""
-    dev = _pool(refs)
-    n = _rows(dev, block_table, "block_table", seq_lens_k=seq_lens_k)
-    n_out = _rows(dev, block_table_out, "block_table_out", parents=parents, seq_lens_out=seq_lens_out)
-    _call("mvp_kv_fork_paged", dev, stream, refs.data_ptr(), refs.shape[0], block_table.data_ptr(),
-          seq_lens_k.data_ptr(), n, block_table.shape[1], parents.data_ptr(), n_out, block_table_out.data_ptr(),
+    num_blocks, b, b_out = refs.numel(), block_table.shape[:1], block_table_out.shape[:1]
+    dev = _checked(refs, num_blocks, "block_table", block_table, None, "seq_lens_k", seq_lens_k, b, "parents", parents,
+                   b_out, "block_table_out", block_table_out, None, "seq_lens_out", seq_lens_out, b_out)
+    _call("mvp_kv_fork_paged", dev, stream, refs.data_ptr(), num_blocks, block_table.data_ptr(), seq_lens_k.data_ptr(),
+          b[0], block_table.shape[1], parents.data_ptr(), b_out[0], block_table_out.data_ptr(),
           block_table_out.shape[1], seq_lens_out.data_ptr(), int(block_size))
 
 
@@ -123,10 +130,11 @@ def kv_trim_paged(refs, block_table, seq_lens_k, new_seq_lens, block_size, *, st
     """Cut requests to ``new_seq_lens`` (0 frees them): their pages past it
     lose a holder, seq_lens_k is written (see ``mvp_kv_trim_paged`` in
     include/mvp.h)."""
-    dev = _pool(refs)
-    n = _rows(dev, block_table, "block_table", seq_lens_k=seq_lens_k, new_seq_lens=new_seq_lens)
-    _call("mvp_kv_trim_paged", dev, stream, refs.data_ptr(), refs.shape[0], block_table.data_ptr(),
-          block_table.shape[1], seq_lens_k.data_ptr(), new_seq_lens.data_ptr(), n, int(block_size))
+    num_blocks, b = refs.numel(), block_table.shape[:1]
+    dev = _checked(refs, num_blocks, "block_table", block_table, None, "seq_lens_k", seq_lens_k, b, "new_seq_lens",
+                   new_seq_lens, b)
+    _call("mvp_kv_trim_paged", dev, stream, refs.data_ptr(), num_blocks, block_table.data_ptr(), block_table.shape[1],
+          seq_lens_k.data_ptr(), new_seq_lens.data_ptr(), b[0], int(block_size))
 
 
 def kv_compact_paged(caches, refs, block_table, seq_lens_k, block_map, num_live, workspace, *, stream=None):
@@ -135,14 +143,11 @@ def kv_compact_paged(caches, refs, block_table, seq_lens_k, block_map, num_live,
     block_map int32 [num_blocks] (each page's new id, -1: free) and num_live
     int32 [1] are written; workspace uint8 of
     ``kv_compact_workspace_size(num_blocks)`` bytes."""
-    dev = _pool(refs, caches.num_blocks)
+    num_blocks, b = caches.num_blocks, block_table.shape[:1]
+    dev = _checked(refs, num_blocks, "block_table", block_table, None, "seq_lens_k", seq_lens_k, b, "block_map",
+                   block_map, (num_blocks,), "num_live", num_live, (1,))
     if caches.device != dev:
         raise ValueError(f"the caches must be on {dev}")
-    n = _rows(dev, block_table, "block_table", seq_lens_k=seq_lens_k)
-    _need(dev, _I32, "block_map", block_map)
-    if block_map.shape != refs.shape:
-        raise ValueError("block_map must be [num_blocks]")
-    _scalar_and_workspace(dev, "num_live", num_live, workspace)
-    _call("mvp_kv_compact_paged", dev, stream, caches.pointers, len(caches.tensors), caches.row_bytes, refs.data_ptr(),
-          caches.num_blocks, block_table.data_ptr(), block_table.shape[1], caches.block_size, seq_lens_k.data_ptr(), n,
-          block_map.data_ptr(), num_live.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _call("mvp_kv_compact_paged", dev, stream, caches.pointers, caches.count, caches.row_bytes, refs.data_ptr(),
+          num_blocks, block_table.data_ptr(), block_table.shape[1], caches.block_size, seq_lens_k.data_ptr(), b[0],
+          block_map.data_ptr(), num_live.data_ptr(), *_workspace(workspace, dev))

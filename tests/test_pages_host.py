@@ -116,7 +116,7 @@ def test_the_tensors_device_is_current_in_the_call(calls, name, call):  # noqa: 
 
 def test_a_pools_caches():
     h = _handle()
-    assert (h.num_blocks, h.block_size, h.row_bytes, len(h.pointers)) == (4, 16, 256, 2)
+    assert (h.num_blocks, h.block_size, h.row_bytes, h.count) == (4, 16, 256, 2)
     h = mvp.kv_caches([FakeTensor((64, 2, 64), torch.float32)], 32)
     assert (h.num_blocks, h.row_bytes) == (2, 512)
     for bad in ([], [FakeTensor((4, 16, 2, 64), BF16), FakeTensor((4, 16, 2, 32), BF16)],
