@@ -799,6 +799,8 @@ size_t mvp_kv_evict_workspace_size(int num_reqs, int num_heads_kv, int budget);
  * block_table   int32 [num_reqs, max_blocks_per_seq].  Ids outside
  *               [0, num_blocks) are left out of every step.
  * block_size    16, 32, 64, 128 or 256.
+ * Rows that were never written are read as masked keys where their page is
+ * (V times a probability of zero): the caches start out finite, all zeros say.
  * Calls on one pool are ordered by the caller (one stream, or events).
  * Errors of all: MVP_ERR_ARG, MVP_ERR_UNSUPPORTED (alignment, row_bytes, more
  * than 256 caches), MVP_ERR_CAPACITY (workspace), MVP_ERR_CUDA.
@@ -813,7 +815,8 @@ size_t mvp_kv_evict_workspace_size(int num_reqs, int num_heads_kv, int budget);
  * start of the call) takes a page in its place first: the filled rows are
  * copied in every cache, and the old page loses a holder (when all its holders
  * append in one call, it is free afterwards).  The new tokens' rows are not
- * written.  At most 65535 requests.
+ * written: this is the step before mvp_rope_append_paged, whose rows then lie
+ * in pages that no other request holds.  At most 65535 requests.
  * missing       int32 device scalar: 0, or the number of pages that the pool
  *               lacks, or -1 when a length is negative or a new length exceeds
  *               max_blocks_per_seq * block_size.  Unless it is 0 nothing is

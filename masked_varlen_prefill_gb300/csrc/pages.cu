@@ -9,10 +9,12 @@
 // first, so that they too give the same result in every run.
 //
 // * extend_plan_kernel: one cluster.  Its first CTA sums up what each request
-//   needs (a prefix sum over the requests), all of them count the free pages of
+//   needs (a prefix sum over the requests), the others count the free pages of
 //   their part of refs; after the cluster's barrier each hands the free pages of
 //   its part, which are consecutive in rank, to the requests that those ranks
-//   belong to.  page_copy_kernel then copies the shared, partly filled pages
+//   belong to (found in shared memory; searched in global memory, and with the
+//   first CTA counting too, 256 requests and 131072 pages took 15 us, 10
+//   now: latency, of four dependent loads and the barriers).  page_copy_kernel then copies the shared, partly filled pages
 //   that a request appends to (copy on write), in every cache.
 // * compact_plan_kernel: one cluster.  Pages past the number of live ones move
 //   to the free ids before it, both in ascending order; compact_move_kernel
@@ -129,12 +131,29 @@ struct ExtendParams {
   int num_blocks, num_reqs, max_blocks, shift;
 };
 
+// The last of n bases that is at most k.
+template <class Base>
+__device__ __forceinline__ int last_at_most(const Base& base, int n, long long k) {
+  int b = 0;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (base(b + half) <= k) {
+      b += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return b;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendParams p) {
   __shared__ long long s_sum[kPlanWarps];
   __shared__ int s_isum[kPlanWarps];
   __shared__ long long s_free[kMaxCluster];  // of every CTA of the cluster
   __shared__ long long s_need;               // pages that the call needs
   __shared__ int s_bad;
+  __shared__ int s_base[kPlanThreads];  // the requests' bases, where they fit
   griddep_launch_dependents();
   const int ctas = static_cast<int>(cluster_ctas());
   const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -191,12 +210,14 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
       }
     }
   }
-  // The free pages of this CTA's part.
-  long long lo, hi;
-  part_of(p.num_blocks, rank, ctas, lo, hi);
-  long long count = 0;
-  for (long long i = lo + 4 * t; i < hi; i += kTile) count += free_of(refs_of(p.refs, i, p.num_blocks));
-  count = block_sum(count, s_sum);
+  // The free pages of this CTA's part (the first of several has none).
+  long long lo = 0, hi = 0, count = 0;
+  if (rank > 0 || ctas == 1) {
+    part_of(p.num_blocks, ctas > 1 ? rank - 1 : 0, ctas > 1 ? ctas - 1 : 1, lo, hi);
+#pragma unroll 4
+    for (long long i = lo + 4 * t; i < hi; i += kTile) count += free_of(refs_of(p.refs, i, p.num_blocks));
+    count = block_sum(count, s_sum);
+  }
   if (t < ctas) {
     if (t == rank) s_free[rank] = count;
     else st_cluster_u64(mapa_shared(smem_u32(&s_free[rank]), t), count);
@@ -218,7 +239,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
     }
     for (int b = t; b < p.num_reqs; b += kPlanThreads) p.new_lens[b] = p.lens[b] + (missing == 0 ? p.add[b] : 0);
   }
-  if (missing != 0) return;
+  if (missing != 0 || at >= need || lo >= hi) return;
+  const bool in_shared = p.num_reqs <= kPlanThreads;
+  if (in_shared) {
+    if (t < p.num_reqs) s_base[t] = p.reqs[t].base;
+    __syncthreads();
+  }
   for (long long i0 = lo; i0 < hi && at < need; i0 += kTile) {
     const long long i = i0 + 4 * t;
     const int4 r = refs_of(p.refs, i, p.num_blocks);
@@ -230,16 +256,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
     for (int j = 0; j < 4; ++j) {
       if (held[j] > 0) continue;
       if (k < need) {
-        int b = 0, n = p.num_reqs;  // the last request whose first new page has a rank of at most k
-        while (n > 1) {
-          const int half = n >> 1;
-          if (p.reqs[b + half].base <= k) {
-            b += half;
-            n -= half;
-          } else {
-            n = half;
-          }
-        }
+        // the last request whose first new page has a rank of at most k
+        const int b = in_shared ? last_at_most([&](int i) { return s_base[i]; }, p.num_reqs, k)
+                                : last_at_most([&](int i) { return p.reqs[i].base; }, p.num_reqs, k);
         const ExtendRequest q = p.reqs[b];
         const int page = static_cast<int>(i) + j;
         p.bt[static_cast<size_t>(b) * p.max_blocks + q.start + (static_cast<int>(k) - q.base)] = page;
@@ -594,7 +613,7 @@ int mvp_kv_extend_paged(void* const* caches, int num_caches, size_t row_bytes, i
   p.num_reqs = num_reqs;
   p.max_blocks = max_blocks_per_seq;
   p.shift = shift;
-  const int ctas = plan_ctas(num_blocks);
+  const int ctas = std::min(kMaxCluster, plan_ctas(num_blocks) + 1);
   if (launch(extend_plan_kernel, ctas, kPlanThreads, ctas, false, stream, ExtendParams(p)) != cudaSuccess) return MVP_ERR_CUDA;
   if (launch(page_copy_kernel, copy_grid(c, num_reqs, num_sms), kCopyThreads, 1, true, stream, Caches(c),
              static_cast<const PageCopy*>(p.copies), static_cast<const int*>(p.n_copies), refs) != cudaSuccess)

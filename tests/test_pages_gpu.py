@@ -353,3 +353,67 @@ def test_bounds_checked_build():
         assert pool.extend([1, 1, 1, 30]) == 0
         pool.trim([0, 21, 0, 33])
         pool.compact()
+
+
+def test_without_requests_nothing_lacks():
+    pool = Pool([20], 12, 16, 4)
+    missing = torch.full((1,), 5, dtype=torch.int32, device=pool.dev)
+    none = pool.d_lens[:0]
+    before = pool.d_refs.clone()
+    mvp.kv_extend_paged(pool.handle, pool.d_refs, pool.d_bt[:0], none, none, none, missing,
+                        torch.empty(0, dtype=torch.uint8, device=pool.dev))
+    mvp.kv_trim_paged(pool.d_refs, pool.d_bt[:0], none, none, 16)
+    assert int(missing) == 0 and torch.equal(before, pool.d_refs)
+
+
+def test_a_captured_batch_change_replays():
+    """Trim, fork and compact in one graph: the same pool, put back as it was, gives the same again."""
+    pool = Pool([40, 17, 100, 5], 60, 16, 8, hkv=1, d=32, seed=12)
+    keep, parents = pool.t32([33, 0, 100, 5]), pool.t32([2, 0, 0, 3, -1])
+    bt, lens = torch.zeros((5, 8), dtype=torch.int32, device=pool.dev), torch.zeros(5, dtype=torch.int32, device=pool.dev)
+    new, live = torch.zeros(60, dtype=torch.int32, device=pool.dev), torch.zeros(1, dtype=torch.int32, device=pool.dev)
+    ws = torch.empty(mvp.kv_compact_workspace_size(60), dtype=torch.uint8, device=pool.dev)
+    state = [t.clone() for t in (pool.d_refs, pool.d_lens, *pool.caches)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mvp.kv_trim_paged(pool.d_refs, pool.d_bt, pool.d_lens, keep, 16)
+        mvp.kv_fork_paged(pool.d_refs, pool.d_bt, pool.d_lens, parents, bt, lens, 16)
+        mvp.kv_compact_paged(pool.handle, pool.d_refs, bt, lens, new, live, ws)
+    op.trim(pool.refs, pool.rows, pool.lens, keep.tolist(), 16)
+    rows, want = op.fork(pool.refs, pool.rows, pool.lens, parents.tolist())
+    new_want, moves, n = op.compact(pool.refs, rows)
+    src, dst = (torch.tensor(x, device=pool.dev) for x in zip(*moves))
+    for c in pool.want:
+        c[dst] = c[src]
+    for _ in range(2):
+        for t, x in zip((pool.d_refs, pool.d_lens, *pool.caches), state):
+            t.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert lens.tolist() == want and int(live) == n and new.tolist() == new_want and pool.d_refs.tolist() == pool.refs
+        assert all(bt[b, :len(row)].tolist() == row for b, row in enumerate(rows))
+        assert all(torch.equal(c, w) for c, w in zip(pool.caches, pool.want))
+
+
+def test_every_step_on_another_stream():
+    """Each step on a stream that waits for nothing but its own inputs, with the current stream kept busy."""
+    pool = Pool([40, 17, 100, 5], 60, 16, 8, seed=13)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.randn((4096, 4096), device=pool.dev)
+    for _ in range(20):
+        busy = busy @ busy * 1e-3
+    bt, lens = torch.zeros((2, 8), dtype=torch.int32, device=pool.dev), torch.zeros(2, dtype=torch.int32, device=pool.dev)
+    parents, keep = pool.t32([2, 2]), pool.t32([0, 90])
+    new, live = torch.zeros(60, dtype=torch.int32, device=pool.dev), torch.zeros(1, dtype=torch.int32, device=pool.dev)
+    ws = torch.empty(mvp.kv_compact_workspace_size(60), dtype=torch.uint8, device=pool.dev)
+    s.wait_stream(torch.cuda.current_stream())
+    mvp.kv_fork_paged(pool.d_refs, pool.d_bt, pool.d_lens, parents, bt, lens, 16, stream=s)
+    mvp.kv_trim_paged(pool.d_refs, bt, lens, keep, 16, stream=s)
+    mvp.kv_compact_paged(pool.handle, pool.d_refs, bt, lens, new, live, ws, stream=s)
+    s.synchronize()
+    rows, n = op.fork(pool.refs, pool.rows, pool.lens, [2, 2])
+    op.trim(pool.refs, rows, n, [0, 90], 16)
+    _, _, want = op.compact(pool.refs, rows)
+    assert int(live) == want and lens.tolist() == n and pool.d_refs.tolist() == pool.refs
+    assert bt[1, :len(rows[1])].tolist() == rows[1]
