@@ -229,7 +229,7 @@ struct Plan {
 // a distance bias the nearest keys weigh most: walked towards them, the running
 // maximum rises in every tile of a head whose bias grows by more than the
 // rescale threshold over a tile, and each rise rescales O (2 x 8192 rows, 32/8
-// heads, D = 128, slopes 2^-0.25 .. 2^-8: 1245 us, BACKTIME backwards).
+// heads, D = 128, slopes 2^-0.25 .. 2^-8: 1245 us, 1041 backwards).
 template <bool FIRST, bool BACK>
 __device__ __forceinline__ int tile_of(const Plan& pl, int j) {
   if constexpr (FIRST) return j < pl.n_first ? j : pl.kb_lo + j - pl.n_first;
@@ -1470,9 +1470,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           acc_e[k] = 0ull;
           acc_lo[k] = acc_hi[k] = 0.f;
         }
-        auto prob_pair = [&](int i, uint64_t t) {
+        uint64_t step2 = 0ull;  // BIAS: of eight columns
+        if constexpr (BIAS) {
+          const float nm = fmaf(-lin * d0, sc, -m_use), step = 8.f * lin * sc;
+          nm2 = f2_pack(nm, nm);
+          step2 = f2_pack(step, step);
+        }
+#pragma unroll
+        for (int i = 0; i < HC / 2; ++i) {
+          if constexpr (BIAS) {
+            if (i > 0 && i % 4 == 0) nm2 = f2_add(nm2, step2);
+          }
           float t0, t1;
-          f2_unpack(t, t0, t1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2), t0, t1);
           const float e0 = ex2_approx(t0);
           const float e1 = ex2_approx(t1);
           const uint32_t pk = pack_bf16x2(e0, e1);
@@ -1480,20 +1490,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             add_bf16x2_halves(pk, acc_lo[i & 3], acc_hi[i & 3]);
           if constexpr (LSE) acc_e[i & 3] = f2_add(acc_e[i & 3], f2_pack(e0, e1));
           s[i] = pk;
-        };
-        auto score_pair = [&](int i) { return f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])); };
-        if constexpr (BIAS) {
-          const float nm = fmaf(-lin * d0, sc, -m_use), step = 8.f * lin * sc;
-          nm2 = f2_pack(nm, nm);
-          const uint64_t step2 = f2_pack(step, step);
-#pragma unroll
-          for (int i = 0; i < HC / 2; ++i) {
-            if (i > 0 && i % 4 == 0) nm2 = f2_add(nm2, step2);
-            prob_pair(i, f2_fma(score_pair(i), sc2, nm2));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < HC / 2; ++i) prob_pair(i, f2_fma(score_pair(i), sc2, nm2));
         }
         {
           float a0, a1, b0, b1;
