@@ -342,11 +342,11 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   if (cap > 0.f && !(rate > 1e-37 && rate < 1e37)) return MVP_ERR_UNSUPPORTED;
   const double u = rate * rate;
   const float tanh2[] = {kTanh2_1, kTanh2_2}, tanh3[] = {kTanh3_1, kTanh3_2, kTanh3_3},
-              tanh4[] = {kTanh1, kTanh2, kTanh3, kTanh4};
+              tanh4[] = {kTanh4_1, kTanh4_2, kTanh4_3, kTanh4_4};
   for (int i = 0; i < 2; ++i) m.sf.near2[i] = static_cast<float>(tanh2[i] * std::pow(u, i + 1));
   for (int i = 0; i < 3; ++i) m.sf.near3[i] = static_cast<float>(tanh3[i] * std::pow(u, i + 1));
   for (int i = 0; i < 4; ++i) m.sf.near4[i] = static_cast<float>(tanh4[i] * std::pow(u, i + 1));
-  const float near[] = {kTanhNear2, kTanhNear3, kTanhNear};
+  const float near[] = {kNear2, kNear3, kNear4};
   // (coefficients past fp32's range: every score takes the other way)
   for (int i = 0; i < 3; ++i) m.sf.cap_near[i] = std::isfinite(m.sf.near4[3]) ? near[i] * m.sf.cap_raw : 0.f;
   m.sf.slopes = scores != nullptr ? scores->distance_slopes : nullptr;

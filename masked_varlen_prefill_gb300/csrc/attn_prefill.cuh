@@ -1364,15 +1364,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const ScoreParams& f = p.m.sf;
             if (near(f.cap_near[0])) poly(kTanh2_0, f.near2[0], f.near2[1]);
             else if (near(f.cap_near[1])) poly(kTanh3_0, f.near3[0], f.near3[1], f.near3[2]);
-            else if (near(f.cap_near[2])) poly(kTanh0, f.near4[0], f.near4[1], f.near4[2], f.near4[3]);
+            else if (near(f.cap_near[2])) poly(kTanh4_0, f.near4[0], f.near4[1], f.near4[2], f.near4[3]);
             else {
+#pragma unroll 1
+              for (int c = 0; c < HC / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld_32x32b_x32(scol + half * HC + c * 32, x);
+                tmem_ld_wait(x);
 #pragma unroll
-              for (int i = 0; i < HC / 2; ++i) {
-                float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
-                cap_scores(x0, x1, f.inv_cap_raw, cap_r);
-                s[2 * i] = __float_as_uint(x0);
-                s[2 * i + 1] = __float_as_uint(x1);
+                for (int i = 0; i < 16; ++i) {
+                  float x0 = __uint_as_float(x[2 * i]), x1 = __uint_as_float(x[2 * i + 1]);
+                  cap_scores(x0, x1, f.inv_cap_raw, cap_r);
+                  x[2 * i] = __float_as_uint(x0);
+                  x[2 * i + 1] = __float_as_uint(x1);
+                }
+                tmem_st_32x32b_x32(scol + half * HC + c * 32, x);
               }
+              tmem_st_wait();
+#pragma unroll
+              for (int c = 0; c < HC / 32; ++c)
+                tmem_ld_32x32b_x32(scol + half * HC + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
+#pragma unroll
+              for (int c = 0; c < HC / 32; ++c) tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
             }
           }
         }

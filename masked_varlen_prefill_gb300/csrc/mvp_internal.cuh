@@ -53,13 +53,19 @@ enum FaultInjection : int { kFaultNone = 0, kFaultWithholdProbs = 1 };
 // units a score x = scale log2(e) q.k becomes c tanh(x / c) with a cap c, and
 // slope[h] log2(e) |p - j| is subtracted.
 // tanh(y) / y for |y| <= T as a polynomial in y^2, minimax in the relative
-// error: of degree 2 for T = 0.25 (4.0e-7), 3 for 0.4 (9.8e-8), 4 for 0.6 (7.3e-8;
-// fp32 arithmetic adds some 1e-7).
-constexpr float kTanhNear2 = 0.25f, kTanhNear3 = 0.4f, kTanhNear = 0.6f;
-constexpr float kTanh2_0 = 0.999999583f, kTanh2_1 = -0.333219081f, kTanh2_2 = 0.128416136f;
-constexpr float kTanh3_0 = 0.999999881f, kTanh3_1 = -0.333313614f, kTanh3_2 = 0.132709771f, kTanh3_3 = -0.0475536026f;
+// error.  Of degree 4 for T = 0.6 (7.3e-8; 1.8e-7 with fp32 arithmetic), and,
+// where the whole of a tile goes through one of them, of degree 2 for T = 0.28
+// (7.7e-7), 3 for 0.5 (5.4e-7) and 4 for 0.75 (5.7e-7): each product less is
+// 6-13 % of the time at D = 128, and the logarithm of a row's sum, fp32, stays
+// within 1e-6 of itself.
+constexpr float kTanhNear = 0.6f;
 constexpr float kTanh0 = 0.99999994f, kTanh1 = -0.333323091f, kTanh2 = 0.133101732f, kTanh3 = -0.0521014817f,
                 kTanh4 = 0.0154754277f;
+constexpr float kNear2 = 0.28f, kNear3 = 0.5f, kNear4 = 0.75f;
+constexpr float kTanh2_0 = 0.999999225f, kTanh2_1 = -0.333155245f, kTanh2_2 = 0.127209172f;
+constexpr float kTanh3_0 = 0.999999464f, kTanh3_1 = -0.333263189f, kTanh3_2 = 0.131902963f, kTanh3_3 = -0.0444022268f;
+constexpr float kTanh4_0 = 0.999999464f, kTanh4_1 = -0.333282501f, kTanh4_2 = 0.132589832f, kTanh4_3 = -0.0500563011f,
+                kTanh4_4 = 0.0129296323f;
 
 struct ScoreParams {
   float cap_log2;         // the cap, times log2(e); 0: none

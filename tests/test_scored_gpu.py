@@ -2,7 +2,7 @@
 documents that do not see each other (GPU), packed and paged, against the
 float64 oracle, with the tolerances of the other attention tests
 (``gpu_helpers.compare``: 1e-2 or two bf16 half steps of the value, lse 1e-3
-relative).  A capped score is off by some 2e-7 of itself and a biased one by half
+relative).  A capped score is off by some 9e-7 of itself and a biased one by half
 an fp32 unit of the bias, 1e-4 at most here: less than either by far."""
 
 import numpy as np
