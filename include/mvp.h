@@ -353,8 +353,9 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
  *
  * softcap         0 (no cap) or 1e-30 .. 1e30, and softcap / scale within
  *                 1e-37 .. 1e37 (MVP_ERR_UNSUPPORTED otherwise).
- * distance_slopes fp32 [num_heads_q], any finite values, or NULL.  Distances
- *                 up to 2^24 are exact.
+ * distance_slopes fp32 [num_heads_q] or NULL: values of either sign whose
+ *                 product with the longest distance, over scale, is finite.
+ *                 Distances up to 2^24 are exact.
  * doc_table       int32 [total_q, 2], 8-byte aligned, or NULL: the closed key
  *                 interval of each row's document (mvp_fill_query_documents).
  *                 A row with an empty interval sees nothing (out = 0).  V of

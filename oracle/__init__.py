@@ -12,6 +12,8 @@ something written independently of it:
   (step14_4 "Causal Mask optimisation" tutorial) OR-ed with the range part
   (PR #50294 mask_mod), and a dense float64 softmax attention with the two sink
   modes of vLLM PR #49815 (MiMo window attention sinks).
+* ``scores``       -- attention with functions of the score and documents.
+* ``pages``        -- a pool's pages, one after another.
 * ``accounting``   -- exact visible-score counts from the dense mask, and the
   per-request ``num_tokens * min(context_len, window)`` estimate of vLLM
   PR #55624 (SWA-aware MFU accounting).
