@@ -64,7 +64,12 @@ __host__ __device__ constexpr int qdl_for(int, int gp) { return gp == 8 ? 8 : 16
 // part of the SMs (beside the prefill kernel) the decode rows of the mixed
 // serving batch ran 11 % faster.  A 64-key tile then holds exactly one step
 // per compute warp.
-__host__ __device__ constexpr int pairs_for(int d, int gp) { return (d == 128 && gp >= 4) ? 2 : 1; }
+// Functions of the score, which a lane computes for its own pairs, make two
+// worth it at D = 64 too, for two or four heads (5 rows of up to 32768 keys, 12/4
+// heads, cap: 56 us with one, 47 with two; for one head 23 and 31).
+__host__ __device__ constexpr int pairs_for(int d, int gp, bool scored) {
+  return (d == 128 && gp >= 4) || (scored && d == 64 && (gp == 2 || gp == 4)) ? 2 : 1;
+}
 
 template <int D>
 struct DCfg {
@@ -130,7 +135,7 @@ template <int D, int GP, bool PAGED, bool FIRST, bool SCORED>
 __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUtensorMap& map_v, const DecodeParams& p) {
   using C = DCfg<D>;
   constexpr int DPL = C::DPL;
-  constexpr int PPL = pairs_for(D, GP);  // probabilities per lane and step
+  constexpr int PPL = pairs_for(D, GP, SCORED);  // probabilities per lane and step
   constexpr int KG = 32 * PPL / GP;      // keys per warp step
   constexpr int NG = C::KT / KG;     // warp steps per tile
   static_assert((C::NW + 1) * GP * (D + 2) * 4 <= C::STAGES * 2 * C::TILE, "merge buffers fit the stages");
@@ -139,7 +144,7 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
   // Per compute warp, the step's 32 probabilities (key kk, head g at
   // kk * GP + g) as (p, p) pairs, read back by every lane as broadcasts
   // instead of 32 shuffles.
-  __shared__ __align__(16) float pbuf[C::NW][64 * pairs_for(D, GP)];
+  __shared__ __align__(16) float pbuf[C::NW][64 * PPL];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ DBarriers sb;
 
