@@ -47,8 +47,12 @@ __host__ __device__ constexpr int kt_for(int d) { return d == 64 ? 128 : (d == 1
 // rows of the mixed serving batches ran at 87 / 82 % of the measured HBM
 // bandwidth against 98 / 90 % with two.  The other head dims keep three: their
 // CTAs are limited by registers, so fewer stages would only shrink the bytes
-// in flight.
-__host__ __device__ constexpr int stages_for(int d) { return d == 128 ? 2 : 3; }
+// in flight.  Functions of the score at D = 64 take two as well, with registers
+// for three CTAs: the functions' latency wants more warps (128 rows of up to 9000
+// keys, 32/8 heads: 314 us with three stages and two CTAs, 301).
+__host__ __device__ constexpr int stages_for(int d, bool scored = false) {
+  return d == 128 || (scored && d == 64) ? 2 : 3;
+}
 __host__ __device__ constexpr int box_for(int d) { return d > 256 ? 256 : d; }
 // Compute warps per CTA (a producer warp comes on top).  Eight at D = 128
 // (two CTAs per SM, 8-dim lane slices to fit the registers) measured slower
@@ -71,14 +75,14 @@ __host__ __device__ constexpr int pairs_for(int d, int gp, bool scored) {
   return (d == 128 && gp >= 4) || (scored && d == 64 && (gp == 2 || gp == 4)) ? 2 : 1;
 }
 
-template <int D>
+template <int D, bool SCORED = false>
 struct DCfg {
   static constexpr int DPL = D / 32;          // dims per lane
   static constexpr int KT = kt_for(D);        // keys per tile
   static constexpr int BOX = box_for(D);
   static constexpr int NBOX = D / BOX;
   static constexpr int TILE = KT * D * 2;     // bytes of one K (or V) tile
-  static constexpr int STAGES = stages_for(D);
+  static constexpr int STAGES = stages_for(D, SCORED);
   static constexpr int SMEM = STAGES * 2 * TILE + 1024;
   static constexpr int NW = nw_for(D);          // compute warps
   static constexpr int THREADS = (NW + 1) * 32;  // + the producer warp
@@ -133,7 +137,7 @@ __device__ __forceinline__ int row_off(int kk, int lane) {
 // its document's keys (each at run time).
 template <int D, int GP, bool PAGED, bool FIRST, bool SCORED>
 __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUtensorMap& map_v, const DecodeParams& p) {
-  using C = DCfg<D>;
+  using C = DCfg<D, SCORED>;
   constexpr int DPL = C::DPL;
   constexpr int PPL = pairs_for(D, GP, SCORED);  // probabilities per lane and step
   constexpr int KG = 32 * PPL / GP;      // keys per warp step
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(DCfg<D>::THREADS)
 // Registers for as many CTAs per SM as shared memory holds (a warp scheduler
 // has room for three warps of up to 168 registers, and a CTA has five warps).
 template <int D, int GP, bool PAGED, bool FIRST>
-__global__ void __launch_bounds__(DCfg<D>::THREADS, D == 512 ? 1 : D == 128 && GP <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(DCfg<D, true>::THREADS, D == 512 ? 1 : D == 64 || (D == 128 && GP <= 4) ? 3 : 2)
     attn_decode_scored_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                               const __grid_constant__ DecodeParams p) {
   decode_rows<D, GP, PAGED, FIRST, true>(map_k, map_v, p);
@@ -690,7 +694,7 @@ cudaError_t launch_dg(const DecodeParams& p, const CUtensorMap& mk, const CUtens
   {
     std::lock_guard<std::mutex> lock(g_decode_attr_mutex);
     if (!attr_set[paged ? 1 : 0][dev]) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DCfg<D>::SMEM);
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DCfg<D, SCORED>::SMEM);
       if (e != cudaSuccess) return e;
       attr_set[paged ? 1 : 0][dev] = true;
     }
@@ -707,12 +711,12 @@ cudaError_t launch_dg(const DecodeParams& p, const CUtensorMap& mk, const CUtens
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(DCfg<D>::THREADS);
-    cfg.dynamicSmemBytes = DCfg<D>::SMEM;
+    cfg.blockDim = dim3(DCfg<D, SCORED>::THREADS);
+    cfg.dynamicSmemBytes = DCfg<D, SCORED>::SMEM;
     cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, kern, mk, mv, p);
   }
-  kern<<<grid, DCfg<D>::THREADS, DCfg<D>::SMEM, stream>>>(mk, mv, p);
+  kern<<<grid, DCfg<D, SCORED>::THREADS, DCfg<D, SCORED>::SMEM, stream>>>(mk, mv, p);
   return cudaGetLastError();
 }
 
