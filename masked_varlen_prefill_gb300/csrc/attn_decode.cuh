@@ -57,7 +57,9 @@ __host__ __device__ constexpr int box_for(int d) { return d > 256 ? 256 : d; }
 // Compute warps per CTA (a producer warp comes on top).  Eight at D = 128
 // (two CTAs per SM, 8-dim lane slices to fit the registers) measured slower
 // than four with three CTAs per SM.
-__host__ __device__ constexpr int nw_for(int) { return 4; }
+// Functions of the score take eight at D = 512, where an SM holds one CTA (64 rows
+// of up to 9000 keys, 8/2 heads: 314 us with four, 289).
+__host__ __device__ constexpr int nw_for(int d, bool scored = false) { return scored && d == 512 ? 8 : 4; }
 // Dims of q and K per lane in the score step (q registers: QDL * GP): 16
 // keeps the reduce-scatter to log2(D / 16) stages; 8-dim slices at D = 128
 // and 4 heads (one more stage, fewer registers) measured ~10 % slower.
@@ -84,7 +86,7 @@ struct DCfg {
   static constexpr int TILE = KT * D * 2;     // bytes of one K (or V) tile
   static constexpr int STAGES = stages_for(D, SCORED);
   static constexpr int SMEM = STAGES * 2 * TILE + 1024;
-  static constexpr int NW = nw_for(D);          // compute warps
+  static constexpr int NW = nw_for(D, SCORED);          // compute warps
   static constexpr int THREADS = (NW + 1) * 32;  // + the producer warp
 };
 
@@ -386,7 +388,18 @@ __device__ __forceinline__ void decode_rows(const CUtensorMap& map_k, const CUte
     const int w0 = w_lo + t * C::KT;
     const int t0 = FIRST && w0 < n_first ? w0 : w0 + skip;
     const bool interior = t0 >= core_lo && t0 + C::KT - 1 <= core_hi;
-    for (int gi = warp; gi < NG; gi += C::NW) {
+    // SCORED: a tile of fewer steps than warps (few heads, few keys) is one group
+    // of warps', the next tile the next group's (the others only pass the stage
+    // on), so that as many tiles are worked on at once as the ring holds.  (56
+    // rows of 6152 keys, 8/8 heads, D = 512, tiles of one step: 1955 us while the
+    // first warp took every tile, 920; 8 rows, 16/8 heads, D = 256: 184 and 125.)
+    constexpr int GROUPS = SCORED && NG < C::NW ? C::NW / NG : 1;
+    if (GROUPS > 1 && t % GROUPS != warp / NG) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.empty[s]);
+      continue;
+    }
+    for (int gi = GROUPS > 1 ? warp % NG : warp; gi < NG; gi += C::NW) {
       float x[NSUB];
 #pragma unroll
       for (int a = 0; a < NSUB; ++a) {
