@@ -219,6 +219,19 @@ def _check_cuda(name, t, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _check_all(device, dtype, *named):
+    """``_check_cuda`` of name, tensor, name, tensor, ... (None: not given),
+    in one pass while nothing is wrong."""
+    if device.type == "cuda":
+        for t in named[1::2]:
+            if t is not None and not (t.dtype is dtype and t.device == device and t.is_contiguous()):
+                break
+        else:
+            return
+    for name, t in zip(named[::2], named[1::2]):
+        _check_cuda(name, t, dtype, device)
+
+
 def fill_query_ranges(ranges, query_start_loc, seq_lens, out, num_tokens, rows_written=None, stream=None):
     """Per-row range table (see ``mvp_fill_query_ranges`` in include/mvp.h).
 
@@ -251,9 +264,8 @@ def fill_query_documents(doc_starts, query_start_loc, seq_lens, out, num_tokens,
     """
     lib = load_library()
     dev = out.device
-    for n, t in (("doc_starts", doc_starts), ("query_start_loc", query_start_loc), ("seq_lens", seq_lens),
-                 ("out", out)):
-        _check_cuda(n, t, torch.int32, dev)
+    _check_all(dev, torch.int32, "doc_starts", doc_starts, "query_start_loc", query_start_loc, "seq_lens", seq_lens,
+               "out", out)
     num_reqs = seq_lens.shape[0]
     if doc_starts is not None and (doc_starts.dim() != 2 or doc_starts.shape[0] != num_reqs):
         raise ValueError("doc_starts must be [num_reqs, max_docs]")
@@ -270,12 +282,14 @@ def _score_options(softcap, distance_slopes, doc_table, num_heads_q, total_q, de
     """``mvp_score_options`` of an attention call, or None when none is given."""
     if softcap == 0 and distance_slopes is None and doc_table is None:
         return None
-    _check_cuda("distance_slopes", distance_slopes, torch.float32, dev)
-    _check_cuda("doc_table", doc_table, torch.int32, dev)
-    if distance_slopes is not None and distance_slopes.shape != (num_heads_q,):
-        raise ValueError("distance_slopes must be [Hq]")
-    if doc_table is not None and doc_table.shape != (total_q, 2):
-        raise ValueError("doc_table must be [total_q, 2]")
+    if distance_slopes is not None:
+        _check_cuda("distance_slopes", distance_slopes, torch.float32, dev)
+        if distance_slopes.shape != (num_heads_q,):
+            raise ValueError("distance_slopes must be [Hq]")
+    if doc_table is not None:
+        _check_cuda("doc_table", doc_table, torch.int32, dev)
+        if doc_table.shape != (total_q, 2):
+            raise ValueError("doc_table must be [total_q, 2]")
     return ctypes.byref(ScoreOptions(float(softcap), _ptr(distance_slopes), _ptr(doc_table)))
 
 
@@ -304,13 +318,10 @@ def attn_fwd_varlen(q, k, v, out, cu_seqlens_q, cu_seqlens_k, max_q_len, max_k_l
     """
     lib = load_library()
     dev = q.device
-    for n, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        _check_cuda(n, t, torch.bfloat16, dev)
-    for n, t in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k), ("context_lens", context_lens),
-                 ("range_table", range_table), ("range_covered", range_covered)):
-        _check_cuda(n, t, torch.int32, dev)
-    _check_cuda("lse", lse, torch.float32, dev)
-    _check_cuda("sinks", sinks, torch.float32, dev)
+    _check_all(dev, torch.bfloat16, "q", q, "k", k, "v", v, "out", out)
+    _check_all(dev, torch.int32, "cu_seqlens_q", cu_seqlens_q, "cu_seqlens_k", cu_seqlens_k, "context_lens",
+               context_lens, "range_table", range_table, "range_covered", range_covered)
+    _check_all(dev, torch.float32, "lse", lse, "sinks", sinks)
     if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or out.shape != q.shape:
@@ -414,13 +425,10 @@ def attn_fwd_paged(q, k_cache, v_cache, out, cu_seqlens_q, seq_lens_k, block_tab
     dev = q.device
     if k_cache.dim() == 4:
         k_cache, v_cache = _rows_of_blocks(k_cache, stream), _rows_of_blocks(v_cache, stream)
-    for n, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
-        _check_cuda(n, t, torch.bfloat16, dev)
-    for n, t in (("cu_seqlens_q", cu_seqlens_q), ("seq_lens_k", seq_lens_k), ("block_table", block_table),
-                 ("context_lens", context_lens), ("range_table", range_table), ("range_covered", range_covered)):
-        _check_cuda(n, t, torch.int32, dev)
-    _check_cuda("lse", lse, torch.float32, dev)
-    _check_cuda("sinks", sinks, torch.float32, dev)
+    _check_all(dev, torch.bfloat16, "q", q, "k_cache", k_cache, "v_cache", v_cache, "out", out)
+    _check_all(dev, torch.int32, "cu_seqlens_q", cu_seqlens_q, "seq_lens_k", seq_lens_k, "block_table", block_table,
+               "context_lens", context_lens, "range_table", range_table, "range_covered", range_covered)
+    _check_all(dev, torch.float32, "lse", lse, "sinks", sinks)
     if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if q.dim() != 3 or k_cache.dim() != 3 or v_cache.shape != k_cache.shape or out.shape != q.shape:

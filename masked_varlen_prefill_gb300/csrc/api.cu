@@ -343,9 +343,13 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   const double u = rate * rate;
   const float tanh2[] = {kTanh2_1, kTanh2_2}, tanh3[] = {kTanh3_1, kTanh3_2, kTanh3_3},
               tanh4[] = {kTanh4_1, kTanh4_2, kTanh4_3, kTanh4_4};
-  for (int i = 0; i < 2; ++i) m.sf.near2[i] = static_cast<float>(tanh2[i] * std::pow(u, i + 1));
-  for (int i = 0; i < 3; ++i) m.sf.near3[i] = static_cast<float>(tanh3[i] * std::pow(u, i + 1));
-  for (int i = 0; i < 4; ++i) m.sf.near4[i] = static_cast<float>(tanh4[i] * std::pow(u, i + 1));
+  double ui = 1.0;
+  for (int i = 0; i < 4; ++i) {
+    ui *= u;
+    if (i < 2) m.sf.near2[i] = static_cast<float>(tanh2[i] * ui);
+    if (i < 3) m.sf.near3[i] = static_cast<float>(tanh3[i] * ui);
+    m.sf.near4[i] = static_cast<float>(tanh4[i] * ui);
+  }
   const float near[] = {kNear2, kNear3, kNear4};
   // (coefficients past fp32's range: every score takes the other way)
   for (int i = 0; i < 3; ++i) m.sf.cap_near[i] = std::isfinite(m.sf.near4[3]) ? near[i] * m.sf.cap_raw : 0.f;
