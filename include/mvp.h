@@ -351,8 +351,9 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
  * the document does, and first_tokens are the request's, seen by rows of the
  * document that holds them.
  *
- * softcap         0 (no cap) or 1e-30 .. 1e30, and softcap / scale within
- *                 1e-37 .. 1e37 (MVP_ERR_UNSUPPORTED otherwise).
+ * softcap         0 (no cap) or 1e-30 .. 1e30 (MVP_ERR_ARG otherwise, NaN
+ *                 too), and softcap / scale within 1e-37 .. 1e37
+ *                 (MVP_ERR_UNSUPPORTED otherwise).
  * distance_slopes fp32 [num_heads_q] or NULL: values of either sign whose
  *                 product with the longest distance, over scale, is finite.
  *                 Distances up to 2^24 are exact.
@@ -364,8 +365,7 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
  * scores          NULL, or with none of the three: the _first call, bit for
  *                 bit.
  * All other arguments, results and errors are those of the _first calls;
- * MVP_ERR_ARG also for a softcap out of range or NaN,
- * MVP_ERR_UNSUPPORTED for a doc_table that is not 8-byte aligned.
+ * MVP_ERR_UNSUPPORTED also for a doc_table that is not 8-byte aligned.
  * mvp_attn_key_weights_* and mvp_attn_accounting know of none of these.
  */
 typedef struct {
@@ -888,7 +888,8 @@ int mvp_get_last_device_error(void* stream);
 const char* mvp_status_str(int status);
 
 /* Number of kernel launches the last successful mvp_attn_* /
- * mvp_fill_query_* / mvp_rope_append_paged / mvp_kv_* call enqueued on this thread (for launch accounting). */
+ * mvp_fill_query_* / mvp_rope_append_paged / mvp_kv_* call enqueued on this
+ * thread (for launch accounting). */
 int mvp_last_launch_count(void);
 
 #ifdef __cplusplus
