@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -350,9 +351,18 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
     if (i < 3) m.sf.near3[i] = static_cast<float>(tanh3[i] * ui);
     m.sf.near4[i] = static_cast<float>(tanh4[i] * ui);
   }
-  const float near[] = {kNear2, kNear3, kNear4};
-  // (coefficients past fp32's range: every score takes the other way)
-  for (int i = 0; i < 3; ++i) m.sf.cap_near[i] = std::isfinite(m.sf.near4[3]) ? near[i] * m.sf.cap_raw : 0.f;
+  // The |q.k| below which each polynomial is taken: its interval, as far as its
+  // coefficients hold in fp32.  One below the smallest normal number may be lost:
+  // then up to 2^(51 / n) (degree n), where it is 2^-126 s^(2n) = 2^-24 of the
+  // factor at most, and the squares are finite.  None past fp32's largest number.
+  // Scores past these bounds take the way that divides by the cap first.
+  const float near[] = {kNear2, kNear3, kNear4}, reach[] = {47453132.f, 131072.f, 6888.f};
+  const double last[] = {kTanh2_2 * u * u, kTanh3_3 * u * u * u, kTanh4_4 * u * u * u * u};
+  for (int i = 0; i < 3; ++i) {
+    m.sf.cap_near[i] = near[i] * m.sf.cap_raw;
+    if (std::fabs(last[i]) < FLT_MIN) m.sf.cap_near[i] = std::min(m.sf.cap_near[i], reach[i]);
+    if (last[2] > FLT_MAX) m.sf.cap_near[i] = 0.f;
+  }
   m.sf.slopes = scores != nullptr ? scores->distance_slopes : nullptr;
   m.sf.docs = scores != nullptr ? scores->doc_table : nullptr;
   m.total_q = total_q;

@@ -72,7 +72,7 @@ struct ScoreParams {
   float inv_cap;          // 1 / cap_log2
   // The prefill kernels' scores stay in units of q.k: the cap is cap_raw = softcap
   // / scale, and the polynomials above take u = s^2 (their first coefficient
-  // needs no scaling); cap_near: the |s| below which each holds.
+  // needs no scaling); cap_near: the |s| below which each is taken.
   float cap_raw, inv_cap_raw;
   float cap_near[3];
   float near2[2], near3[3], near4[4];
