@@ -338,10 +338,23 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
   m.sf.cap_log2 = cap * 1.4426950408889634f;
   m.sf.inv_cap = cap > 0.f ? 1.f / m.sf.cap_log2 : 0.f;
   const double rate = cap > 0.f ? static_cast<double>(scale) / cap : 0.0;
-  m.sf.inv_cap_raw = static_cast<float>(rate);
-  m.sf.cap_raw = cap > 0.f ? static_cast<float>(1.0 / rate) : 0.f;
   if (cap > 0.f && !(rate > 1e-37 && rate < 1e37)) return MVP_ERR_UNSUPPORTED;
-  const double u = rate * rate;
+  m.sf.wide = cap * 1.4426950408889634 > kWideCap;
+  m.sf.unit_log2 = m.scale_log2;
+  m.sf.unit = scale;
+  double part = 1.0;
+  if (m.sf.wide) {
+    int e;
+    std::frexp(scale * 1.4426950408889634, &e);
+    const double unit = std::ldexp(1.0, std::min(e, 127));
+    part = scale * 1.4426950408889634 / unit;
+    m.sf.unit_log2 = static_cast<float>(unit);
+    m.sf.unit = static_cast<float>(unit * 0.6931471805599453);
+  }
+  m.sf.part = static_cast<float>(part);
+  m.sf.inv_cap_raw = static_cast<float>(rate / part);
+  m.sf.cap_raw = cap > 0.f ? static_cast<float>(part / rate) : 0.f;
+  const double u = rate / part * (rate / part);
   const float tanh2[] = {kTanh2_1, kTanh2_2}, tanh3[] = {kTanh3_1, kTanh3_2, kTanh3_3},
               tanh4[] = {kTanh4_1, kTanh4_2, kTanh4_3, kTanh4_4};
   double ui = 1.0;
@@ -351,7 +364,7 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
     if (i < 3) m.sf.near3[i] = static_cast<float>(tanh3[i] * ui);
     m.sf.near4[i] = static_cast<float>(tanh4[i] * ui);
   }
-  // The |q.k| below which each polynomial is taken: its interval, as far as its
+  // The |s| below which each polynomial is taken: its interval, as far as its
   // coefficients hold in fp32.  One below the smallest normal number may be lost:
   // then up to 2^(51 / n) (degree n), where it is 2^-126 s^(2n) = 2^-24 of the
   // factor at most, and the squares are finite.  None past fp32's largest number.

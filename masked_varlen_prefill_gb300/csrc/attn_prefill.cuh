@@ -74,7 +74,7 @@ constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr unsigned kFullMask = 0xffffffffu;
 // Bits of the kernel's SCORE argument.
-constexpr int kScored = 1, kCapped = 2, kBiased = 4;
+constexpr int kScored = 1, kCapped = 2, kBiased = 4, kWide = 8;
 
 template <int D_, int DV_, int BN_, int KST_, int VST_, int NCTA_, int SPLITD_ = 0, int NS_ = 2, int ROWSUM_ = 0>
 struct Cfg {
@@ -509,12 +509,14 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, uint
 // SCORE: functions of the score (kScored bits): rows see only their document's
 // keys, and scores may go through a cap and a distance bias (each at run time;
 // an instantiation without a bit has none of its code: with all of it, documents
-// alone cost 15 % of the time on whole prompts at D = 128).
+// alone cost 15 % of the time on whole prompts at D = 128; kWide: caps past
+// kWideCap, whose products cost the others 4 % where they test for them).
 template <class C, bool PAGED, bool LSE, bool FIRST, int SCORE>
 __global__ void __launch_bounds__(C::THREADS, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const PrefillParams p) {
-  constexpr bool SCORED = SCORE != 0, CAP = (SCORE & kCapped) != 0, BIAS = (SCORE & kBiased) != 0;
+  constexpr bool SCORED = SCORE != 0, CAP = (SCORE & kCapped) != 0, BIAS = (SCORE & kBiased) != 0,
+                 WIDE = (SCORE & kWide) != 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Barriers sb;
@@ -1132,7 +1134,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int half = (warp - C::SOFTMAX_BEGIN) / 4;  // which column half of the row
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const float sc = p.m.scale_log2;  // > 0 (checked on the host)
+    const float sc = WIDE ? p.m.sf.unit_log2 : p.m.scale_log2;  // > 0 (checked on the host)
     const bool key0_mode = p.m.sink_mode == 1 && p.m.sinks != nullptr;
     const bool null_mode = p.m.sink_mode == 2 && p.m.sinks != nullptr;
     float2* xslots = reinterpret_cast<float2*>(smem + C::RED_OFF);
@@ -1177,7 +1179,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if constexpr (SCORED) l.doc = valid ? doc_entry(p.m, e.it.q0 + qi) : make_int2(0, INT_MAX);
       if constexpr (BIAS) {
         l.slope = (!e.last && p.m.sf.slopes != nullptr)
-                      ? __ldg(p.m.sf.slopes + e.it.h0 + (row % p.gpack)) / p.m.scale
+                      ? __ldg(p.m.sf.slopes + e.it.h0 + (row % p.gpack)) / (WIDE ? p.m.sf.unit : p.m.scale)
                       : 0.f;
       }
       return l;
@@ -1217,7 +1219,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // SCORED: no row of this warp sees a key ahead of it
       const bool behind = BIAS && __all_sync(kFullMask, max(vis.b_hi, vis.r_hi) <= cur.it.ctx + rc.qi);
       const float sink_l2 = rc.sink * 1.4426950408889634f;  // log2 units
-      const float sink_raw = rc.sink / p.m.scale;            // units of the raw q.k score
+      const float sink_raw = rc.sink / (WIDE ? p.m.sf.unit : p.m.scale);  // units of the raw q.k score
       float m_ref = null_mode ? sink_l2 : -INFINITY;
       // Partial row sums of this thread's columns: the bf16-rounded
       // probabilities (they normalise O, which the PV MMA builds from them;
@@ -1324,6 +1326,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // tile is a chain of waits that every instruction lengthens).
         if constexpr (CAP) {
           if (p.m.sf.cap_log2 > 0.f) {
+            if constexpr (WIDE) {
+#pragma unroll
+              for (int i = 0; i < HC; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * p.m.sf.part);
+            }
             if (masked) {  // masked scores, which may be anything, do not decide how the others are capped
 #pragma unroll
               for (int w = 0; w < HC / 32; ++w) {
@@ -1375,6 +1381,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 uint32_t x[32];
                 tmem_ld_32x32b_x32(scol + half * HC + c * 32, x);
                 tmem_ld_wait(x);
+                if constexpr (WIDE) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f.part);
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   float x0 = __uint_as_float(x[2 * i]), x1 = __uint_as_float(x[2 * i + 1]);
@@ -1401,9 +1411,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if constexpr (BIAS) {
           // Distances are exact (below 2^24), so a bias is within half a unit in
           // its last place.  Rows of this warp that see no key ahead of them
-          // take distances as they are (a masked key's may be negative).
+          // take distances as they are (a masked key's may be negative).  (WIDE: the
+          // group's distance would be lost beside scores of any size.)
           d0 = static_cast<float>(cur.it.ctx + rc.qi - (kb * BN + half * HC));
-          if (behind || __all_sync(kFullMask, d0 >= static_cast<float>(HC - 1))) {
+          if (!WIDE && (behind || __all_sync(kFullMask, d0 >= static_cast<float>(HC - 1)))) {
             lin = rc.slope;
 #pragma unroll
             for (int i = 0; i < HC / 2; ++i) {

@@ -20,6 +20,7 @@ cudaError_t launch_prefill_docs(int head_dim, const PrefillParams& p, const CUte
 cudaError_t launch_prefill_scored(int head_dim, const PrefillParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
                                   const CUtensorMap& mv, cudaStream_t stream) {
   const bool cap = p.m.sf.cap_log2 > 0.f, bias = p.m.sf.slopes != nullptr;
+  if (p.m.sf.wide) return launch_prefill_scored_wide(head_dim, p, mq, mk, mv, stream);
   if (p.m.first_tokens > 0) return launch_prefill_scored_first(head_dim, p, mq, mk, mv, stream);
   if (cap && bias) return launch_prefill_capped_biased(head_dim, p, mq, mk, mv, stream);
   if (cap) return launch_prefill_capped(head_dim, p, mq, mk, mv, stream);

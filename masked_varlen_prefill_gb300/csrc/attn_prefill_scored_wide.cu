@@ -1,0 +1,21 @@
+// Prefill attention under a cap past kWideCap, with or without any other function
+// of the score and first tokens: instantiations of
+// attn_prefill.cuh.  Translation units of their own, like
+// attn_prefill_first.cu, so that the others stay what they are and all
+// compile in parallel.
+#include "attn_prefill.cuh"
+
+namespace mvp {
+
+cudaError_t launch_prefill_scored_wide(int head_dim, const PrefillParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                                       const CUtensorMap& mv, cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_cfg<Cfg64, true, kScored | kCapped | kBiased | kWide>(p, mq, mk, mv, stream);
+    case 128: return launch_cfg<Cfg128, true, kScored | kCapped | kBiased | kWide>(p, mq, mk, mv, stream);
+    case 256: return launch_cfg<Cfg256, true, kScored | kCapped | kBiased | kWide>(p, mq, mk, mv, stream);
+    case 512: return launch_cfg<Cfg512, true, kScored | kCapped | kBiased | kWide>(p, mq, mk, mv, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace mvp

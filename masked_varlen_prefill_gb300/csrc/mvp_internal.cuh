@@ -67,12 +67,23 @@ constexpr float kTanh3_0 = 0.999999464f, kTanh3_1 = -0.333263189f, kTanh3_2 = 0.
 constexpr float kTanh4_0 = 0.999999464f, kTanh4_1 = -0.333282501f, kTanh4_2 = 0.132589832f, kTanh4_3 = -0.0500563011f,
                 kTanh4_4 = 0.0129296323f;
 
+// The prefill kernels round a row's largest score times scale_log2 and take it
+// from the others' products, which are not rounded: scores past some 2^31 in log2
+// units come out above it by more than fp32's exponent holds.  Caps past this bound
+// go to kernels that multiply the scores by a `part` first, which leaves
+// the exponent a power of two, whose products are exact.
+constexpr double kWideCap = 16777216.0;  // in log2 units
+
 struct ScoreParams {
   float cap_log2;         // the cap, times log2(e); 0: none
   float inv_cap;          // 1 / cap_log2
-  // The prefill kernels' scores stay in units of q.k: the cap is cap_raw = softcap
-  // / scale, and the polynomials above take u = s^2 (their first coefficient
-  // needs no scaling); cap_near: the |s| below which each is taken.
+  // The prefill kernels' capped scores stay in units of q.k, or of q.k part under a
+  // wide cap: s times unit_log2 is the score in log2 units, times `unit` (scale, or
+  // the same) the score.  The cap is cap_raw = softcap / unit, and the polynomials
+  // above take u = s^2 (their first coefficient needs no scaling); cap_near: the
+  // |s| below which each is taken.
+  bool wide;
+  float part, unit, unit_log2;
   float cap_raw, inv_cap_raw;
   float cap_near[3];
   float near2[2], near3[3], near4[4];
@@ -173,6 +184,7 @@ MVP_LAUNCH_PREFILL(launch_prefill_capped);
 MVP_LAUNCH_PREFILL(launch_prefill_biased);
 MVP_LAUNCH_PREFILL(launch_prefill_capped_biased);
 MVP_LAUNCH_PREFILL(launch_prefill_scored_first);
+MVP_LAUNCH_PREFILL(launch_prefill_scored_wide);
 #undef MVP_LAUNCH_PREFILL
 
 // ----------------------------------------------------------------- decode

@@ -57,6 +57,9 @@ RANGES = [
     # factors of s^2 whose powers leave fp32's range below
     (30.0, 1e-4, 0.74), (30.0, 1e-5, 0.49), (30.0, 1e-5, 0.74), (30.0, 1e-6, 0.49), (30.0, 1e-6, 0.74),
     (30.0, 1e-8, 0.27), (30.0, 1e-8, 0.74), (30.0, 1e-10, 0.27), (30.0, 1e-10, 0.49), (30.0, 1e-12, 2.0),
+    # squares that leave it above
+    (1e20, 0.125, 0.27), (1e25, 0.125, 0.27), (1e25, 0.125, 0.74), (1e30, 0.125, 0.49), (1e30, 1.0, 1e-8),
+    (1e30, 1.0, 1e-14), (1e30, 1e-6, 0.01),
     # factors that leave it above
     (1e-3, 1e3, 0.74), (1e-3, 1e3, 0.27), (1e-20, 1e6, 0.49), (1e-2, 1e2, 0.74),
     # and none that does
@@ -77,6 +80,19 @@ def test_caps_over_scales_with_a_bias(cap, scale, top):
     _check(case, cap, top, more=0.1 * cap * 16 * 2.0 ** -24)
 
 
-@pytest.mark.parametrize("cap,scale,top", RANGES[:10])
+@pytest.mark.parametrize("cap,scale,top", RANGES[:17])
 def test_caps_over_scales_under_first_tokens(cap, scale, top):
     _check(_case(64, cap, scale, top, seed=2, window=50, first=5), cap, top)
+
+
+@pytest.mark.parametrize("window", [-1, 50])
+@pytest.mark.parametrize("cap,scale,top", RANGES[10:17])
+def test_wide_caps_with_a_bias(cap, scale, top, window):
+    """(Keys whose sums of score and bias nearly meet: which of them wins is open, their log-sum-exp is not.)"""
+    case = _case(128, cap, scale, top, seed=3, window=window, slopes=cap * top / 3000 * np.array([1.0, 0.5, -0.25, 0.0]))
+    out, lse = case.run()
+    want = case.oracle()[1]
+    err = np.abs(lse.double().cpu().numpy() - want)
+    assert torch.isfinite(out).all() and (out.abs() <= case.v.abs().amax() * (1 + 2.0 ** -7)).all()
+    assert err.max() <= 4e-6 * cap * np.tanh(top) * 1.2, (err.max(), cap)
+    assert same((out, lse), case.run(16))
