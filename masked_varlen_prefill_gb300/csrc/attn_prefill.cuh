@@ -73,6 +73,9 @@ namespace {
 constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr unsigned kFullMask = 0xffffffffu;
+// Biased scores, log2 units: what a gentle slope adds over a thread's columns at
+// most, and the size from which a maximum is kept above all roundings.
+constexpr float kGentleBias = 1024.0f, kLargeBiased = 67108864.0f;
 // Bits of the kernel's SCORE argument.
 constexpr int kScored = 1, kCapped = 2, kBiased = 4, kWide = 8;
 
@@ -1151,7 +1154,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int f_hi;  // FIRST: last visible first token, or -1
       float sink;
       int f_lo;     // SCORED: first visible first token
-      float slope;  // SCORED: distance bias per key, q.k units
+      float slope;  // BIAS: distance bias per key, q.k units
     };
     const int pos_off = row_pos_off();
     // p_full lives in rank 0: one arrival per warp (released at cluster scope in a pair)
@@ -1167,7 +1170,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int2 tab;
       float sink;
       int2 doc;     // SCORED
-      float slope;  // SCORED
+      float slope;  // BIAS
     };
     auto row_loads = [&](const PlanEntry& e) {
       RowLoads l;
@@ -1216,8 +1219,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const Plan& pl = cur.pl;
       const RowVis vis = rc.vis;
       const int f_hi = rc.f_hi;
-      // SCORED: no row of this warp sees a key ahead of it
-      const bool behind = BIAS && __all_sync(kFullMask, max(vis.b_hi, vis.r_hi) <= cur.it.ctx + rc.qi);
+      // BIAS: no row of this warp sees a key ahead of it, and their slopes are gentle
+      const bool behind = BIAS && !WIDE && __all_sync(kFullMask, max(vis.b_hi, vis.r_hi) <= cur.it.ctx + rc.qi &&
+                                                                     fabsf(rc.slope) * sc * HC <= kGentleBias);
       const float sink_l2 = rc.sink * 1.4426950408889634f;  // log2 units
       const float sink_raw = rc.sink / (WIDE ? p.m.sf.unit : p.m.scale);  // units of the raw q.k score
       float m_ref = null_mode ? sink_l2 : -INFINITY;
@@ -1406,15 +1410,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // Distance bias.  Behind the row it is -slope (d0 - i) at column i, d0 the
         // first column's distance: slope (i % 8) is added to the scores here, and
         // -lin (d0 - 8 g), the same for eight columns, to their maximum and in the
-        // exponent (one packed add per pair of scores).
+        // exponent (one packed add per pair of scores).  Some 13 roundings of 2^-24 of
+        // slope d0, or of the maximum if that is larger (slope / scale, its products, a
+        // group's step, the exponent's FFMA): under gentle slopes 8e-4 in log2 units
+        // at most for the keys of the row's own tile, under steep ones, where d0 is 2 HC
+        // or more, 2^-19 of the bias itself.  Nearer keys of steep slopes, and keys
+        // ahead, take their own biases, each rounded once with its score: a row's own
+        // key then has none, however steep the slope.
         float d0 = 0.f, lin = 0.f;
         if constexpr (BIAS) {
-          // Distances are exact (below 2^24), so a bias is within half a unit in
-          // its last place.  Rows of this warp that see no key ahead of them
-          // take distances as they are (a masked key's may be negative).  (WIDE: the
-          // group's distance would be lost beside scores of any size.)
+          // (Distances are exact below 2^24.  Rows of this warp that see no key ahead
+          // of them take distances as they are: a masked key's may be negative.  WIDE:
+          // a group's bias would be lost beside scores of any size.)
           d0 = static_cast<float>(cur.it.ctx + rc.qi - (kb * BN + half * HC));
-          if (!WIDE && (behind || __all_sync(kFullMask, d0 >= static_cast<float>(HC - 1)))) {
+          if (!WIDE && (behind || __all_sync(kFullMask, d0 >= static_cast<float>(2 * HC)))) {
             lin = rc.slope;
 #pragma unroll
             for (int i = 0; i < HC / 2; ++i) {
@@ -1486,10 +1495,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         float alpha = 1.f;
         const bool need = (mx > m_ref + kRescaleThreshold) || (m_ref == -INFINITY && mx > -INFINITY);
         if (need) {
-          alpha = ex2_approx(m_ref - mx);  // 0 when m_ref == -inf
+          // BIAS: a maximum past 2^26 is taken larger than the scores' roundings, or they
+          // might come out above it by more than fp32's exponent holds (tiles of
+          // far keys under steep slopes, which a later tile leaves behind)
+          float m = mx;
+          if (BIAS && !WIDE && fabsf(mx) > kLargeBiased) m = fmaf(fabsf(mx), 0x1p-20f, mx);
+          alpha = ex2_approx(m_ref - m);  // 0 when m_ref == -inf
           l_sum *= alpha;
           l_lse *= alpha;
-          m_ref = mx;
+          m_ref = m;
         }
         const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
         const uint64_t sc2 = f2_pack(sc, sc);
