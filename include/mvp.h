@@ -824,8 +824,8 @@ size_t mvp_kv_evict_workspace_size(int num_reqs, int num_heads_kv, int budget);
  * in pages that no other request holds.  At most 65535 requests.
  * missing       int32 device scalar: 0, or the number of pages that the pool
  *               lacks, or -1 when a length is negative or a new length exceeds
- *               max_blocks_per_seq * block_size.  Unless it is 0 nothing is
- *               changed, and new_seq_lens is seq_lens_k.
+ *               max_blocks_per_seq * block_size or 2^31 - 1.  Unless it is 0
+ *               nothing is changed, and new_seq_lens is seq_lens_k.
  * workspace     device scratch of mvp_kv_extend_workspace_size bytes, 16-byte
  *               aligned, no initialisation needed.  Two calls that may run at
  *               the same time need separate workspaces.

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
       bool cow = false;
       if (b < p.num_reqs) {
         const long long n = p.lens[b], a = p.add[b];
-        if (n < 0 || a < 0 || ((n + a + (1LL << p.shift) - 1) >> p.shift) > p.max_blocks) {
+        if (n < 0 || a < 0 || n + a > INT_MAX || ((n + a + (1LL << p.shift) - 1) >> p.shift) > p.max_blocks) {
           bad = true;
         } else {
           start = pages_of(n, p.shift);

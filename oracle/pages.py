@@ -16,7 +16,7 @@ def pages_of(n, block):
 
 def extend(refs, rows, lens, add, block, max_pages):
     """(missing, copies): rows, lens and refs are changed unless missing."""
-    if any(n < 0 or a < 0 or pages_of(n + a, block) > max_pages for n, a in zip(lens, add)):
+    if any(n < 0 or a < 0 or n + a > 2 ** 31 - 1 or pages_of(n + a, block) > max_pages for n, a in zip(lens, add)):
         return -1, []
     need = []
     for row, n, a in zip(rows, lens, add):
