@@ -847,7 +847,8 @@ size_t mvp_kv_extend_workspace_size(int num_reqs);
  * a row with c continuations gain c - 1 holders, so those of a row that
  * nothing continues lose one.  Entries past a request's pages are not written.
  * The new arrays do not overlap the old ones, whose rows no longer hold pages
- * afterwards.
+ * afterwards.  At most 2^24 rows each, num_reqs * num_out at most 2^40
+ * (MVP_ERR_UNSUPPORTED): each row of the old batch reads all parents.
  */
 int mvp_kv_fork_paged(int32_t* refs, int num_blocks, const int32_t* block_table, const int32_t* seq_lens_k,
                       int num_reqs, int max_blocks_per_seq, const int32_t* parents, int num_out,

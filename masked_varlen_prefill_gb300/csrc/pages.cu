@@ -648,6 +648,8 @@ int mvp_kv_fork_paged(int32_t* refs, int num_blocks, const int32_t* block_table,
   if (shift < 0 || num_reqs < 0 || num_out < 0 || num_blocks < 1 || max_blocks_per_seq < 1) return MVP_ERR_ARG;
   if (max_blocks_out < max_blocks_per_seq) return MVP_ERR_ARG;
   if (num_reqs > (1 << 24) || num_out > (1 << 24)) return MVP_ERR_UNSUPPORTED;
+  // (each old row reads all parents: the kernel would hold the GPU for minutes)
+  if (static_cast<long long>(num_reqs) * num_out > 1LL << 40) return MVP_ERR_UNSUPPORTED;
   if (num_reqs + num_out == 0) return MVP_OK;
   if (refs == nullptr || (num_reqs > 0 && (block_table == nullptr || seq_lens_k == nullptr))) return MVP_ERR_ARG;
   if (num_out > 0 && (parents == nullptr || block_table_out == nullptr || seq_lens_out == nullptr)) return MVP_ERR_ARG;
