@@ -8,11 +8,11 @@
 // (4 bytes a page, against the thousands of bytes a page holds), lowest ids
 // first, so that they too give the same result in every run.
 //
-// * extend_plan_kernel: one cluster.  Its first CTA sums up what each request
-//   needs (a prefix sum over the requests), the others count the free pages of
-//   their part of refs; after the cluster's barrier each hands the free pages of
-//   its part, which are consecutive in rank, to the requests that those ranks
-//   belong to.  page_copy_kernel then copies the shared, partly filled pages
+// * extend_plan_kernel: one cluster of two CTAs or more.  Its first sums up what
+//   each request needs (a prefix sum over the requests), the others count the free
+//   pages of their part of refs; after the cluster's barrier each hands the free
+//   pages of its part, which are consecutive in rank, to the requests that those
+//   ranks belong to.  page_copy_kernel then copies the shared, partly filled pages
 //   that a request appends to (copy on write), in every cache.
 // * compact_plan_kernel: one cluster.  Pages past the number of live ones move
 //   to the free ids before it, both in ascending order; compact_move_kernel
@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
   __shared__ int s_base[kPlanThreads];  // the requests' bases, where they fit
   griddep_launch_dependents();
   const int ctas = static_cast<int>(cluster_ctas());
-  const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int rank = static_cast<int>(cluster_rank());
   const int t = threadIdx.x;
-  if (ctas > 1) cluster_sync_all();  // every CTA runs: its shared memory may be written
+  cluster_sync_all();  // every CTA runs: its shared memory may be written
 
   // What each request needs (the first CTA).
   if (rank == 0) {
@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
       }
     }
   }
-  // The free pages of this CTA's part (the first of several has none).
+  // The free pages of this CTA's part (the first has none).
   long long lo = 0, hi = 0, count = 0;
-  if (rank > 0 || ctas == 1) {
-    part_of(p.num_blocks, ctas > 1 ? rank - 1 : 0, ctas > 1 ? ctas - 1 : 1, lo, hi);
+  if (rank > 0) {
+    part_of(p.num_blocks, rank - 1, ctas - 1, lo, hi);
 #pragma unroll 4
     for (long long i = lo + 4 * t; i < hi; i += kTile) count += free_of(refs_of(p.refs, i, p.num_blocks));
     count = block_sum(count, s_sum);
@@ -223,8 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendP
     if (t == rank) s_free[rank] = count;
     else st_cluster_u64(mapa_shared(smem_u32(&s_free[rank]), t), count);
   }
-  if (ctas > 1) cluster_sync_all();
-  else __syncthreads();
+  cluster_sync_all();
 
   long long total = 0, at = 0;
   for (int r = 0; r < ctas; ++r) {
