@@ -504,7 +504,6 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
         dp.cluster = static_cast<int>(std::min<long long>(8, parts / splits));
         while ((dp.cluster & (dp.cluster - 1)) != 0) --dp.cluster;
         dp.n_splits = splits;
-        dp.partial = splits > 1 ? static_cast<float*>(partials) : nullptr;
         dp.min_chunk = kFirstChunk;
       }
     }
