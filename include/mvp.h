@@ -358,9 +358,10 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
  *                 product with the longest distance, over scale, is finite.
  *                 Distances up to 2^24 are exact; a bias is an fp32 number, off
  *                 by less than 2^-19 of itself (and 1e-3, or 2^-20 of the row's
- *                 largest score).  The largest biased score of a prompt's row
- *                 lies within 4e7 of 0 (the nearest visible key's under
- *                 a positive slope: any slope does for rows that see themselves).
+ *                 largest score).  In a prompt's row the key that counts most
+ *                 has a bias within 4e7 of 0, and its biased score is above
+ *                 -4e7 (the nearest visible key under a positive slope: any
+ *                 slope does for rows that see themselves).
  * doc_table       int32 [total_q, 2], 8-byte aligned, or NULL: the closed key
  *                 interval of each row's document (mvp_fill_query_documents).
  *                 A row with an empty interval sees nothing (out = 0).  V of

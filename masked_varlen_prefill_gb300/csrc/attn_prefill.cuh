@@ -74,8 +74,8 @@ constexpr int kBM = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr unsigned kFullMask = 0xffffffffu;
 // Biased scores, log2 units: what a gentle slope adds over a thread's columns at
-// most, and the size from which a maximum is kept above all roundings.
-constexpr float kGentleBias = 1024.0f, kLargeBiased = 67108864.0f;
+// most, and below which a maximum is kept above all roundings.
+constexpr float kGentleBias = 1024.0f, kLeastBiased = -67108864.0f;
 // Bits of the kernel's SCORE argument.
 constexpr int kScored = 1, kCapped = 2, kBiased = 4, kWide = 8;
 
@@ -1495,11 +1495,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         float alpha = 1.f;
         const bool need = (mx > m_ref + kRescaleThreshold) || (m_ref == -INFINITY && mx > -INFINITY);
         if (need) {
-          // BIAS: a maximum past 2^26 is taken larger than the scores' roundings, or they
+          // BIAS: a maximum below -2^26 is taken larger than the scores' roundings, or they
           // might come out above it by more than fp32's exponent holds (tiles of
-          // far keys under steep slopes, which a later tile leaves behind)
+          // far keys under steep slopes, which a later tile leaves behind; by
+          // its sign, so that large scores keep theirs)
           float m = mx;
-          if (BIAS && !WIDE && fabsf(mx) > kLargeBiased) m = fmaf(fabsf(mx), 0x1p-20f, mx);
+          if (BIAS && !WIDE && mx < kLeastBiased) m = mx * (1.f - 0x1p-20f);
           alpha = ex2_approx(m_ref - m);  // 0 when m_ref == -inf
           l_sum *= alpha;
           l_lse *= alpha;

@@ -81,3 +81,17 @@ def test_biases_of_any_size_leave_averages(cap):
     want = case.oracle()[1]
     err = np.abs(lse.double().cpu().numpy() - want)
     assert (err <= 2.0 ** -20 * np.abs(want) + 6.0).all(), err.max()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_large_scores_under_gentle_slopes(d):
+    """Scores of up to 2e8 (multiples of one vector, so that each is exact): the row's largest keeps its weight."""
+    w = W("t", 45, [150, 1], [300, 290], 4, 2, d, True, -1, 0, NONE, None, 0.125)
+    case = Case(w, slopes=[0.5, 0.01, -0.1, 0.0])
+    case.k = torch.ones_like(case.k) * (1 + torch.arange(590, device=case.dev) % 97)[:, None, None].bfloat16()
+    case.q = torch.full_like(case.q, 2.0 ** 17 * 128 / d)
+    out, lse = case.run()
+    want = case.oracle()[1]
+    err = np.abs(lse.double().cpu().numpy() - want)
+    assert np.abs(want).max() > 1e8 and (err <= 2.0 ** -21 * np.abs(want) + 8.0).all(), err.max()  # (+ ln of equals)
+    assert torch.isfinite(out).all() and same((out, lse), case.run(32))
