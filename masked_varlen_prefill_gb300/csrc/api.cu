@@ -488,15 +488,17 @@ int attn_fwd_impl(const void* q, void* out, float* lse, const int32_t* cu_seqlen
     dp.min_chunk = dp.chunk;
     if (m.sf.any()) {
       // Functions of the score: rows that leave SMs idle are split into 2, 4, 8,
-      // .. parts of kFirstChunk keys or more, as many as the GPU holds CTAs (a
-      // tenth more, which even out rows of different length).  Up to eight parts
-      // are a cluster, which joins them without workspace; past that, clusters
-      // are joined like the splits.  One row, 32/8 heads, D = 128, 32768 keys: 8
-      // splits 82 us, 4 clusters of 8 35, 8 clusters of 7 48 (clusters of other
-      // sizes fill the GPU worse); 5 rows of up to 32768, 12/4 heads, D = 64: 66,
-      // 56 and 67.
+      // .. parts of kFirstChunk keys or more, as many as the GPU's shared memory
+      // holds CTAs (a tenth more, which even out rows of different length).  Up to
+      // eight parts are a cluster, which joins them without workspace; past that,
+      // clusters are joined like the splits.  One row, 32/8 heads, D = 128, 32768
+      // keys: 8 splits 82 us, 4 clusters of 8 35, 8 clusters of 7 48 (clusters of
+      // other sizes fill the GPU worse).  Counting three CTAs per SM, not two, at D =
+      // 64, 7 rows of 9000 .. 32768 keys, 16/4 heads: 65 and 55 us, 3 rows, 16/8: 45
+      // and 34; at D = 128 with eight heads a CTA, where registers are for two, 7
+      // rows, 32/4: 140 with three, 171 with two.
       const long long rows = decode_count * head_ctas;
-      const long long held = static_cast<long long>(num_sms) * decode_ctas_per_sm(head_dim);
+      const long long held = static_cast<long long>(num_sms) * scored_ctas_per_sm(head_dim);
       long long parts = 1;
       while (2 * parts * rows * 10 <= held * 11 && 2 * parts * kFirstChunk <= span + kFirstChunk - 1) parts *= 2;
       if (parts > splits) {

@@ -215,7 +215,8 @@ cudaError_t launch_decode_scored_first(int head_dim, const DecodeParams& p, cons
                                        const CUtensorMap& map_v, cudaStream_t stream, int* launches);
 int decode_keys_per_tile(int head_dim);
 int decode_box_inner(int head_dim);
-int decode_ctas_per_sm(int head_dim);  // that shared memory holds
+// CTAs of the kernels for functions of the score that an SM's shared memory holds.
+int scored_ctas_per_sm(int head_dim);
 // Heads one decode CTA handles for a GQA group of `group` query heads.
 inline int decode_heads_per_cta(int head_dim, int group) {
   if (group == 1) return 1;
