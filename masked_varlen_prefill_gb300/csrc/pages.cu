@@ -562,10 +562,12 @@ cudaError_t launch(void (*kernel)(Args...), int grid, int block, int cluster, bo
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Copying CTAs: so many per SM, or as many as there can be units.  One fewer
-// than a multiple of the units of a page, so that each CTA takes all parts of
-// pages in turn: pages that are copied in part end before their last parts (32
-// prompts shared by 8 samples, 32 caches: 131 us with 1216 CTAs, 112 with 1215).
+// Copying CTAs: so many per SM, or as many as there can be units.  One fewer, so
+// that their number has no power of two in common with the parts of a page and each
+// CTA takes all parts of pages in turn: pages that are copied in part end before
+// their last parts (32 prompts shared by 8 samples, 32 caches, pages of 8 parts: 131
+// us with 1216 CTAs, 112 with 1215).  1215 = 3^5 5: of pages of 3, 5, 6, .. parts a
+// CTA still takes some parts only.
 // A step's extension, which mostly copies nothing, takes eight (a launch that
 // finds no work then costs 2.5 us); a compaction 64 (2 GB moved: 645 us with 8,
 // 606 with 16, 595 with 64: units go to whichever SM is free).

@@ -400,7 +400,7 @@ __device__ __forceinline__ uint64_t grid_launch_id() {
   return r;
 }
 
-// 16-byte store to shared memory of a CTA in this cluster (address from mapa).
+// Shared memory of a CTA in this cluster (addresses from mapa), and how many it has.
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -414,6 +414,7 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
+// 16-byte store to shared memory of a CTA in this cluster (address from mapa).
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
