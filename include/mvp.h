@@ -369,6 +369,9 @@ int mvp_attn_fwd_paged_first(const void* q, const void* k_cache, const void* v_c
  *                 visible key must be finite, as for any masked key.
  * scores          NULL, or with none of the three: the _first call, bit for
  *                 bit.
+ * Prompt rows multiply probabilities rounded to bf16 with V, single tokens
+ * unrounded ones, as in the plain calls.  Without a cap the scores of prompt rows
+ * lie within 1e9 of 0, as there; with one they may have any size.
  * All other arguments, results and errors are those of the _first calls;
  * MVP_ERR_UNSUPPORTED also for a doc_table that is not 8-byte aligned.
  * mvp_attn_key_weights_* and mvp_attn_accounting know of none of these.
