@@ -1500,7 +1500,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           // far keys under steep slopes, which a later tile leaves behind; by
           // its sign, so that large scores keep theirs)
           float m = mx;
-          if (BIAS && !WIDE && mx < kLeastBiased) m = mx * (1.f - 0x1p-20f);
+          if (BIAS && !WIDE && mx < kLeastBiased && (!FIRST || p.m.sf.slopes != nullptr)) m = mx * (1.f - 0x1p-20f);
           alpha = ex2_approx(m_ref - m);  // 0 when m_ref == -inf
           l_sum *= alpha;
           l_lse *= alpha;

@@ -83,6 +83,19 @@ def test_biases_of_any_size_leave_averages(cap):
     assert (err <= 2.0 ** -20 * np.abs(want) + 6.0).all(), err.max()
 
 
+def test_large_negative_scores_under_first_tokens():
+    """Documents under first tokens, without slopes: a row's largest score may be far below 0."""
+    w = W("t", 46, [150, 1], [300, 290], 4, 2, 128, True, 60, 0, NONE, None, 0.125)
+    case = Case(w, first=3, starts=[[], []])
+    case.k = torch.ones_like(case.k) * (60 + torch.arange(590, device=case.dev) % 67)[:, None, None].bfloat16()
+    case.q = torch.full_like(case.q, -(2.0 ** 17))
+    out, lse = case.run()
+    want = case.oracle()[1]
+    err = np.abs(lse.double().cpu().numpy() - want)
+    assert want.max() < -1e8 and (err <= 2.0 ** -21 * np.abs(want) + 8.0).all(), err.max()
+    assert torch.isfinite(out).all() and same((out, lse), case.run(32))
+
+
 @pytest.mark.parametrize("d", [64, 128, 256, 512])
 def test_large_scores_under_gentle_slopes(d):
     """Scores of up to 2e8 (multiples of one vector, so that each is exact): the row's largest keeps its weight."""
