@@ -1325,7 +1325,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
         // Capped and biased scores, still in q.k units.  2 x 8192 rows, 32/8 heads, D
         // = 128: 837 us plain, 1193 with a cap (1320 where the scores ask for degree
-        // 3, 2257 where none is far below the cap), 972 with a bias, 1383 with both;
+        // 3, 2257 where none is far below the cap), 970 with a bias, 1390 with both;
         // the softmax warps bound all of them (44 % of the issue slots in use: each
         // tile is a chain of waits that every instruction lengthens).
         if constexpr (CAP) {
